@@ -335,6 +335,175 @@ int ssm_ssd_fwd(const void *x, const void *dt, const float *dt_bias, int softplu
                 ssm_stream_t stream);
 
 /*
+ * Operators around the Mamba-2 SSD on packed sequences.
+ *
+ * A Mamba-2 block projects its input to rows [z | x B C | dt], passes x B C
+ * through a short causal convolution, runs the SSD over the heads and normalises
+ * the gated result.  The entry points below take time-major rows of packed
+ * sequences: row t of a tensor is a token, rows are `*_stride` elements apart (so
+ * a slice of a wider row needs no copy), and sequence i is rows
+ * cu_seqlens[i] .. cu_seqlens[i + 1] - 1.
+ *
+ *   cu_seqlens     [sequences + 1] int32 on the device, ascending, within
+ *                  [0, tokens]; a sequence may be empty.  Rows behind the last
+ *                  sequence are left as they were in every output.
+ *   slots          optional [sequences] int32 on the device: the row of the cache
+ *                  (windows, states) that belongs to each sequence (NULL: sequence
+ *                  i's is i).  A slot outside [0, slots) stands for none: the
+ *                  sequence starts from zeros and leaves nothing.  Two sequences
+ *                  of one call must not share a slot (which of them leaves its
+ *                  values there is not defined).
+ *   has_initial    optional [sequences] bytes on the device: non-zero where the
+ *                  sequence goes on from its cache row (NULL: every sequence
+ *                  starts from zeros).
+ * The cache row of a sequence that is not empty is updated in place.  An empty
+ * sequence leaves its cache row as it was.  Values outside these ranges in the
+ * device tables never lead to an access out of range.
+ */
+
+/* Sizes of a convolution call. */
+typedef struct {
+    int64_t tokens;    /* rows (packed tokens; for a step, sequences), >= 1 */
+    int64_t dim;       /* channels, >= 1 */
+    int64_t sequences; /* of cu_seqlens, >= 1 (ignored by the step) */
+    int64_t slots;     /* rows of the cache `windows` */
+    int64_t x_stride, y_stride, dy_stride, dx_stride; /* elements between rows, >= dim */
+    int32_t width;     /* K, 1..4 */
+    int32_t silu;      /* non-zero: y = silu(u); zero: y = u */
+    int32_t act_dtype; /* ssm_dtype_t of x, y, dy, dx and windows */
+} ssm_conv1d_dims_t;
+
+/* Sizes of a packed SSD call or of a step. */
+typedef struct {
+    int64_t tokens;    /* rows (packed tokens; for a step, sequences), >= 1 */
+    int64_t sequences; /* of cu_seqlens, >= 1 (ignored by the step) */
+    int64_t slots;     /* rows of the cache `states` */
+    int64_t heads;     /* H, >= 1, a multiple of groups */
+    int64_t headdim;   /* P per head; 64 is supported */
+    int64_t groups;    /* G groups of heads sharing B and C */
+    int64_t dstate;    /* N; 128 is supported */
+    int64_t x_stride, dt_stride, b_stride, c_stride, y_stride; /* elements between rows */
+    int32_t act_dtype; /* ssm_dtype_t; the packed forward supports SSM_BF16, the step both */
+} ssm_ssd_packed_dims_t;
+
+/* Sizes of a gated norm call. */
+typedef struct {
+    int64_t rows;      /* >= 1 */
+    int64_t dim;       /* columns, a multiple of groups; dim / groups at most 16384 */
+    int64_t groups;    /* parts of a row that are normalised alone, >= 1 */
+    int64_t x_stride, z_stride, dout_stride, out_stride, dx_stride, dz_stride; /* elements between rows, >= dim */
+    float eps;
+    int32_t gate_first; /* non-zero: norm(x silu(z)); zero: norm(x) silu(z) */
+    int32_t act_dtype;  /* ssm_dtype_t of every tensor but weight, rstd and dweight */
+} ssm_norm_dims_t;
+
+/*
+ * The short causal depthwise convolution on packed sequences:
+ *
+ *   u_t[c] = bias[c] + sum_{k<K} w[c][k] x_{t-K+1+k}[c],   y = silu(u) (or u)
+ *
+ * where rows before the sequence's first are the K - 1 stored inputs of its
+ * window (oldest first), or zeros.
+ *
+ *   x, y           required, rows of `dim` elements
+ *   w, bias        required [dim][K], optional [dim] float32
+ *   windows        optional [slots][K-1][dim]: read where has_initial is set, and
+ *                  left holding each sequence's last K-1 inputs
+ * Alignment: element size; with 16-byte aligned pointers, and dim and strides of
+ * whole 16-byte vectors, rows are moved as such vectors.  Outputs (y, windows)
+ * overlap no input and not each other.
+ */
+int ssm_conv1d_fwd(const void *x, const float *w, const float *bias, const int32_t *cu_seqlens, void *windows,
+                   const int32_t *slots, const uint8_t *has_initial, void *y, const ssm_conv1d_dims_t *dims,
+                   ssm_stream_t stream);
+
+/*
+ * One token per sequence: row b of x (dims->tokens rows) through the window of
+ * its slot (slots NULL: row b's slot is b, and tokens must not exceed slots),
+ * which is read and moved on by one input in place.  windows is required when
+ * K > 1.  A row whose slot is outside the cache is padding: its row of y is left
+ * as it was.
+ */
+int ssm_conv1d_step(void *windows, const int32_t *slots, const void *x, const float *w, const float *bias, void *y,
+                    const ssm_conv1d_dims_t *dims, ssm_stream_t stream);
+
+/*
+ * Gradients of ssm_conv1d_fwd on sequences that start from zeros, given dy:
+ * dx in the activation dtype, dw [dim][K] and dbias (optional, [dim]) float32,
+ * summed in a fixed order (equal calls give equal bits).  Rows of dx behind the
+ * last sequence are left as they were.  workspace: at least
+ * ssm_conv1d_bwd_workspace_size bytes, 16-byte aligned.
+ */
+int ssm_conv1d_bwd_workspace_size(const ssm_conv1d_dims_t *dims, size_t *bytes);
+int ssm_conv1d_bwd(const void *x, const float *w, const float *bias, const int32_t *cu_seqlens, const void *dy,
+                   void *dx, float *dw, float *dbias, void *workspace, size_t workspace_bytes,
+                   const ssm_conv1d_dims_t *dims, ssm_stream_t stream);
+
+/*
+ * Mamba-2 SSD (the recurrence of ssm_ssd_fwd) over packed sequences, with
+ * float32 states in cache slots.
+ *
+ *   x, y           [tokens][heads][64] bf16, rows x_stride and y_stride apart
+ *   dt             [tokens][heads] bf16, rows dt_stride apart
+ *   B, C           [tokens][groups][128] bf16, rows b_stride and c_stride apart
+ *   A, dt_bias, D  [heads] float32 (dt_bias and D optional)
+ *   states         optional [slots][heads][64][128] float32: read where
+ *                  has_initial is set, and left holding each sequence's state
+ *   workspace      at least ssm_ssd_varlen_fwd_workspace_size bytes, not used by
+ *                  a concurrent call; ssm_scan_fwd_status reads its error word,
+ *                  and returns SSM_ERR_INVALID_ARG when cu_seqlens did not ascend
+ *                  within [0, tokens] (the call then wrote nothing)
+ * Alignment: x, B, C, y, states and workspace 16 bytes, and the strides of x, B,
+ * C and y multiples of 8 elements; dt its element size.  A value that is not
+ * finite in a sequence may spread to the 128 steps around it.  Sequences of more
+ * than 1024 tokens are walked in segments of 1024 (more when tokens exceed 2^20)
+ * that may run on different SMs, the state passing through the workspace; results
+ * do not depend on that.
+ */
+int ssm_ssd_varlen_fwd_workspace_size(const ssm_ssd_packed_dims_t *dims, size_t *bytes);
+int ssm_ssd_varlen_fwd(const void *x, const void *dt, const float *dt_bias, int softplus, const float *A,
+                       const void *B, const void *C, const float *D, const int32_t *cu_seqlens, float *states,
+                       const int32_t *slots, const uint8_t *has_initial, void *y, void *workspace,
+                       size_t workspace_bytes, const ssm_ssd_packed_dims_t *dims, ssm_stream_t stream);
+
+/*
+ * One token of the SSD for every row b of a decode batch (dims->tokens rows),
+ * against the state of its slot, read and updated in place (slots NULL: row b's
+ * slot is b, and tokens must not exceed slots).  A row whose slot is outside the
+ * cache is padding: its row of out is left as it was.  Activations bf16 or
+ * float32; out's rows are y_stride apart.  Alignment: states 16 bytes; B and C
+ * four elements, their strides multiples of four; the rest its element size.
+ */
+int ssm_ssd_step(float *states, const int32_t *slots, const void *x, const void *dt, const float *dt_bias,
+                 int softplus, const float *A, const void *B, const void *C, const float *D, void *out,
+                 const ssm_ssd_packed_dims_t *dims, ssm_stream_t stream);
+
+/*
+ * RMS norm fused with the block's gate, s = silu(z) (s = 1 when z == NULL), over
+ * each of the `groups` equal parts of a row:
+ *
+ *   gate_first:  v = x s,  out = v r w        else:  v = x,  out = v r w s
+ *   r = 1 / sqrt(mean(v^2) + eps)
+ *
+ *   weight         required [dim] float32
+ *   rstd           optional [rows][groups] float32: receives r
+ * Alignment: element size; vector accesses as for ssm_conv1d_fwd.
+ */
+int ssm_gated_norm_fwd(const void *x, const void *z, const float *weight, void *out, float *rstd,
+                       const ssm_norm_dims_t *dims, ssm_stream_t stream);
+
+/*
+ * Gradients of ssm_gated_norm_fwd given dout: dx and dz (required with z) in the
+ * activation dtype, dweight [dim] float32, summed in a fixed order (equal calls
+ * give equal bits).  The statistics are formed again from x and z.  workspace:
+ * at least ssm_gated_norm_bwd_workspace_size bytes, 16-byte aligned.
+ */
+int ssm_gated_norm_bwd_workspace_size(const ssm_norm_dims_t *dims, size_t *bytes);
+int ssm_gated_norm_bwd(const void *x, const void *z, const float *weight, const void *dout, void *dx, void *dz,
+                       float *dweight, void *workspace, size_t workspace_bytes, const ssm_norm_dims_t *dims,
+                       ssm_stream_t stream);
+
+/*
  * ssm_scan_fwd without a workspace.  The pages have no counterpart: this
  * entry point exists for callers that cannot allocate any device memory while
  * they run the scan, not even a workspace (code running inside an allocator or
@@ -386,6 +555,18 @@ int ssm_debug_ssd_flag_timeout(const void *x, const void *dt, const float *dt_bi
                                const float *h0, void *y, float *h_last, void *workspace,
                                size_t workspace_bytes, uint32_t spin_limit, const ssm_ssd_dims_t *dims,
                                ssm_stream_t stream);
+
+/*
+ * Test support, not part of the operation: ssm_ssd_varlen_fwd where every later
+ * segment of a sequence waits for a hand-off flag value that no flag ever reaches
+ * and gives up after `spin_limit` polls (0: at once).  The kernel still ends
+ * normally; ssm_scan_fwd_status then reports SSM_ERR_TIMEOUT.
+ */
+int ssm_debug_ssd_varlen_flag_timeout(const void *x, const void *dt, const float *dt_bias, int softplus,
+                                      const float *A, const void *B, const void *C, const float *D,
+                                      const int32_t *cu_seqlens, float *states, const int32_t *slots,
+                                      const uint8_t *has_initial, void *y, void *workspace, size_t workspace_bytes,
+                                      uint32_t spin_limit, const ssm_ssd_packed_dims_t *dims, ssm_stream_t stream);
 
 /* Static, human-readable text for an SSM_* code (never NULL). */
 const char *ssm_strerror(int code);

@@ -83,6 +83,7 @@ def _load():
     lib.ssm_strerror.restype = ctypes.c_char_p
     lib.ssm_version.argtypes = []
     lib.ssm_version.restype = I
+    mamba2.bind(lib)
     return lib
 
 
@@ -97,7 +98,7 @@ def get_lib():
     return _lib
 
 
-EXPORTS = ("ssm_scan_fwd_workspace_size", "ssm_scan_fwd", "ssm_scan_fwd_status", "ssm_scan_step",
+_EXPORTS = ("ssm_scan_fwd_workspace_size", "ssm_scan_fwd", "ssm_scan_fwd_status", "ssm_scan_step",
            "ssm_conv_scan_fwd", "ssm_conv_scan_step", "ssm_trap_scan_fwd", "ssm_trap_scan_step",
            "ssm_scan_bwd_workspace_size", "ssm_scan_bwd", "ssm_ssd_fwd_workspace_size", "ssm_ssd_fwd",
            "ssm_scan_fwd_noalloc",
@@ -533,6 +534,14 @@ def ssm_scan_step(state, x, delta, delta_bias, softplus, A, B, C, D=None, z=None
     return out
 
 
+from . import mamba2  # noqa: E402  (needs the helpers above)
+from .mamba2 import (Conv1dDims, NormDims, SsdPackedDims, ssm_conv1d_bwd, ssm_conv1d_fwd, ssm_conv1d_step,  # noqa: E402
+                     ssm_gated_norm_bwd, ssm_gated_norm_fwd, ssm_ssd_step, ssm_ssd_varlen_fwd)
+
+EXPORTS = _EXPORTS + mamba2.EXPORTS
+
 __all__ = ["ssm_scan_fwd", "ssm_scan_fwd_workspace_size", "ssm_scan_fwd_status", "ssm_scan_step",
            "ssm_conv_scan_fwd", "ssm_conv_scan_step", "ssm_trap_scan_fwd", "ssm_trap_scan_step", "ssm_scan_bwd",
-           "ssm_ssd_fwd", "ssm_ssd_fwd_workspace_size", "SsdDims", "ssm_strerror", "ssm_version", "SSMError", "Dims", "LIB_PATH", "get_lib"]
+           "ssm_ssd_fwd", "ssm_ssd_fwd_workspace_size", "ssm_ssd_varlen_fwd", "ssm_ssd_step", "ssm_conv1d_fwd",
+           "ssm_conv1d_bwd", "ssm_conv1d_step", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd", "SsdDims", "SsdPackedDims",
+           "Conv1dDims", "NormDims", "ssm_strerror", "ssm_version", "SSMError", "Dims", "LIB_PATH", "get_lib"]

@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB_NAME = "libssm_scan_b200.so"
 LIB_PATH = os.path.join(LIB_DIR, LIB_NAME)
-SOURCES = ["ssm_scan.cu"]
+SOURCES = ["ssm_scan.cu", "mamba2.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -35,7 +35,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         newest = max(os.path.getmtime(f) for f in _inputs())
         if os.path.getmtime(LIB_PATH) >= newest:
             return LIB_PATH
-    cmd = [NVCC, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [NVCC, *ARCH, "-t", "0", "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
            "-I", INCLUDE, "-I", CSRC, "-o", LIB_PATH + ".tmp",
            *[os.path.join(CSRC, s) for s in SOURCES]]
     if verbose:

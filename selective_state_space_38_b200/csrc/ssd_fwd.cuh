@@ -35,17 +35,13 @@
 
 #include <cuda.h>
 
-#include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace ssm {
 
 constexpr int kSsdQ = 128;  // chunk length
-constexpr int kSsdP = 64;   // head dimension
-constexpr int kSsdN = 128;  // state dimension
 constexpr int kSsdConsumers = 256;               // epilogue threads (8 warps)
 constexpr int kSsdThreads = kSsdConsumers + 32;  // + the producer warp
-constexpr uint32_t kSsdWaitLimit = 1u << 24;
-constexpr uint32_t kSsdFlagLimit = 1u << 20;  // polls of a hand-off flag, 64 ns apart at least
 
 // TMA maps, rank 4 with the innermost dimension first: x [P][H][L][batch],
 // B and C [N][G][L][batch]; every box is 64 elements x 1 x 128 steps x 1.
@@ -153,120 +149,6 @@ struct SsdSmem {
 };
 static_assert(SsdSmem::kTotal <= 227 * 1024, "shared memory of the SSD kernel");
 
-__device__ __forceinline__ uint32_t ssd_sw128(int r, int e) {  // byte offset of (row r, element e)
-    const int c = e >> 3, w = (e & 7) * 2;
-    return r * 128 + (((c ^ (r & 7)) << 4) | w);
-}
-
-// Shared-memory matrix descriptor: 128-byte swizzle, sm_100 descriptor version.
-__device__ __forceinline__ uint64_t ssd_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16) |
-           (static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(2) << 61);
-}
-
-// Instruction descriptor: bf16 x bf16 -> f32, M x N, operand majors (0 = K, 1 = MN).
-__host__ __device__ constexpr uint32_t ssd_idesc(int M, int N, int a_mn, int b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a_mn) << 15) |
-           (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
-           (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// D (TMEM) (+)= A (shared memory) B (shared memory)
-__device__ __forceinline__ void ssd_mma(uint32_t d_tmem, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(da), "l"(db), "r"(idesc), "r"(acc), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
-        : "memory");
-}
-
-// D (TMEM) (+)= A (TMEM: lane = row, two bf16 per column, lower index in the
-// low half) B (shared memory)
-__device__ __forceinline__ void ssd_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t db, uint32_t idesc,
-                                           uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(db), "r"(idesc), "r"(acc), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
-        : "memory");
-}
-
-__device__ __forceinline__ void ssd_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-
-// 16 consecutive float32 columns of this thread's TMEM lane
-__device__ __forceinline__ void ssd_ld16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// 16 consecutive 32-bit columns of this thread's TMEM lane from registers
-__device__ __forceinline__ void ssd_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-// 4-D tiled TMA load of a box at (c0, c1, c2, c3); completion as bytes on the mbarrier.
-__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int c0, int c1, int c2, int c3,
-                                            uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-        : "memory");
-}
-
-__device__ __forceinline__ bool ssd_try(uint32_t addr, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
-// Bounded wait for a phase of an mbarrier; gives up early once another wait
-// of the launch has given up (the error word is non-zero).
-__device__ __forceinline__ bool ssd_wait(uint64_t *bar, uint32_t parity, uint32_t *error) {
-    const uint32_t addr = smem_u32(bar);
-    for (uint32_t n = 0; n < kSsdWaitLimit; ++n) {
-        if (ssd_try(addr, parity)) return true;
-        if ((n & 1023u) == 1023u && *reinterpret_cast<volatile uint32_t *>(error) != 0) return false;
-    }
-    atomicOr(error, 2u);
-    return false;
-}
-// The same wait before the CTA may exit with a load or an MMA in flight: it does
-// not stop early on the error word.
-__device__ __forceinline__ void ssd_drain(uint64_t *bar, uint32_t parity, uint32_t *error) {
-    const uint32_t addr = smem_u32(bar);
-    for (uint32_t n = 0; n < kSsdWaitLimit; ++n)
-        if (ssd_try(addr, parity)) return;
-    atomicOr(error, 2u);
-}
-
-// v = hi + lo with hi = bf16(v) and lo = bf16(v - hi), for two values at once:
-// the high parts and the low parts as bf16 pairs (first value in the low half).
-__device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16x2(a, b);
-    lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
-}
-
 // Barrier 1 among the kSsdConsumers epilogue threads (the producer warp is not
 // part of it): a plain sync, and one that returns the AND of a predicate.
 __device__ __forceinline__ void ssd_cbar() { asm volatile("bar.sync 1, %0;" ::"n"(kSsdConsumers) : "memory"); }
@@ -280,10 +162,6 @@ __device__ __forceinline__ bool ssd_cbar_and(bool v) {
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void ssd_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // grid: one CTA per range of units (SsdRange); block: kSsdConsumers epilogue
 // threads and one producer warp.  Epilogue thread (quad, half, lane) owns row
 // 32 quad + lane of every [128][..] tile (its TMEM lane) and the half `half` of

@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include "ssm_scan.h"
+#include "host.h"
 #include "common.cuh"
 #include "scan_fwd.cuh"
 #include "scan_step.cuh"
@@ -26,43 +27,15 @@
 namespace {
 
 using namespace ssm;
+using namespace ssm_host;
 
 constexpr int kVersion = 10000;  // 1.0.0
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-struct Span {
-    const void *p;
-    size_t bytes;
-};
-
-bool overlap(const Span &a, const Span &b) {
-    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
 
 // sizes must be positive and every buffer must stay well inside int64 byte offsets
 bool dims_ok(int64_t batch, int64_t seqlen, int64_t dim) {
     if (batch < 1 || seqlen < 1 || dim < 1) return false;
     const double elems = static_cast<double>(batch) * static_cast<double>(seqlen) * static_cast<double>(dim);
     return elems < 4.0e18 / 16.0;
-}
-
-// cuTensorMapEncodeTiled from the driver, looked up once through the runtime
-// (no link-time dependency on libcuda).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    });
-    return fn;
 }
 
 // A rank-3 [d2][d1][d0] tensor (d0 contiguous) with a [1][box1][box0] box.
@@ -177,15 +150,6 @@ int launch_fwd_kernels(FwdParams p, void *scratch, int64_t segs, int sms, cudaSt
     p.mode = kFromStart;
     p.pass = 1;
     return launch_pass<T, VEC, CONV, TRAP, STATES>(p, sc, tm, sms, stream);
-}
-
-// SMs of the current device (the schedule, and so the workspace size, depend on it)
-int current_sms(int *sms) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || *sms < 1)
-        return SSM_ERR_CUDA;
-    return SSM_OK;
 }
 
 // Workspace bytes of a validated shape on a GPU with `sms` SMs.
@@ -853,5 +817,5 @@ extern "C" int ssm_scan_fwd_status(const void *workspace, ssm_stream_t stream) {
     uint32_t err = 0;
     if (cudaMemcpy(&err, view.error, sizeof err, cudaMemcpyDeviceToHost) != cudaSuccess)
         return SSM_ERR_CUDA;
-    return err ? SSM_ERR_TIMEOUT : SSM_OK;
+    return err & 4u ? SSM_ERR_INVALID_ARG : err ? SSM_ERR_TIMEOUT : SSM_OK;
 }
