@@ -6,6 +6,8 @@
 #include <algorithm>
 #include <climits>
 #include <cstring>
+#include <initializer_list>
+#include <type_traits>
 
 #include "ssm_scan.h"
 #include "host.h"
@@ -437,22 +439,27 @@ int64_t var_pairs(const ssm_ssd_packed_dims_t *d) {
     return d->groups * ((d->heads / d->groups + kVarHeads - 1) / kVarHeads);
 }
 
-// Workspace: [0, 256) header, the list, the flags, then (16-byte aligned) the carried states.
+// Workspace: [0, 256) header, the list, the flags, the decays, then (16-byte aligned) the carried states.
 size_t var_layout(const ssm_ssd_packed_dims_t *d, uint8_t *base, VarWork *w) {
     const int64_t windows = (d->tokens + var_segment(d->tokens) - 1) / var_segment(d->tokens);
     size_t at = 256;
     const size_t list = at;
     at += static_cast<size_t>(windows) * sizeof(int2);
     const size_t flags = at;
-    at = (at + static_cast<size_t>(windows) * var_pairs(d) * 4 + 255) / 256 * 256;
-    const size_t carry = at;
+    at += static_cast<size_t>(windows) * var_pairs(d) * 4;
+    const size_t decay = at;
+    if (windows > 1) at += static_cast<size_t>(windows) * d->heads * 4;
+    const size_t carry = at = (at + 255) / 256 * 256;
     if (windows > 1) at += static_cast<size_t>(windows) * d->heads * kSsdP * kSsdN * 4;  // no carries within one segment
     if (w) {
         w->queue = reinterpret_cast<uint32_t *>(base);
-        w->extras = reinterpret_cast<uint32_t *>(base + 4);
+        w->extras = reinterpret_cast<uint32_t *>(base + 8);
+        w->several = reinterpret_cast<uint32_t *>(base + 12);
         w->error = reinterpret_cast<uint32_t *>(base + 16);
+        w->parallel = reinterpret_cast<uint32_t *>(base + 20);
         w->list = reinterpret_cast<int2 *>(base + list);
         w->flags = reinterpret_cast<uint32_t *>(base + flags);
+        w->decay = reinterpret_cast<float *>(base + decay);
         w->carry = reinterpret_cast<float *>(base + carry);
     }
     return at;
@@ -461,7 +468,7 @@ size_t var_layout(const ssm_ssd_packed_dims_t *d, uint8_t *base, VarWork *w) {
 int ssd_varlen_impl(const void *x, const void *dt, const float *dt_bias, int softplus, const float *A, const void *B,
                     const void *C, const float *D, const int32_t *cu_seqlens, float *states, const int32_t *slots,
                     const uint8_t *has_initial, void *y, void *workspace, size_t workspace_bytes,
-                    const ssm_ssd_packed_dims_t *dims, ssm_stream_t stream, uint32_t bias, uint32_t spin_limit) {
+                    const ssm_ssd_packed_dims_t *dims, ssm_stream_t stream, uint32_t flag_want, uint32_t spin_limit) {
     const int rc = ssd_setup(x, dt, dt_bias, A, B, C, D, slots, y, dims);
     if (rc != SSM_OK) return rc;
     if (dims->act_dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
@@ -493,7 +500,7 @@ int ssd_varlen_impl(const void *x, const void *dt, const float *dt_bias, int sof
     p.heads = static_cast<int32_t>(H), p.groups = static_cast<int32_t>(G), p.pairs = static_cast<int32_t>(var_pairs(dims));
     p.segment = static_cast<int32_t>(var_segment(T));
     p.windows = static_cast<int32_t>((T + p.segment - 1) / p.segment);
-    p.flag_want_bias = bias, p.spin_limit = spin_limit, p.softplus = softplus ? 1 : 0;
+    p.flag_want = flag_want, p.spin_limit = spin_limit, p.softplus = softplus ? 1 : 0;
     var_layout(dims, static_cast<uint8_t *>(workspace), &p.work);
     const int64_t items = (dims->sequences + p.windows) * p.pairs;  // at most
     if (items > INT32_MAX) return SSM_ERR_UNSUPPORTED;
@@ -504,11 +511,19 @@ int ssd_varlen_impl(const void *x, const void *dt, const float *dt_bias, int sof
         return SSM_ERR_CUDA;
     int sms = 0;
     if (current_sms(&sms) != SSM_OK) return SSM_ERR_CUDA;
-    if (cudaFuncSetAttribute(ssd_varlen_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, VarSmem::kTotal) != cudaSuccess)
+    p.sms = sms;
+    if (cudaFuncSetAttribute(ssd_varlen_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, VarSmem::kTotal) != cudaSuccess ||
+        cudaFuncSetAttribute(ssd_varlen_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, VarSmem::kTotal) != cudaSuccess)
         return SSM_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(items, sms));
     ssd_varlen_setup_kernel<<<1, 1024, 0, s>>>(p);
-    ssd_varlen_kernel<<<static_cast<unsigned>(std::min<int64_t>(items, sms)), kVarThreads, VarSmem::kTotal, s>>>(p, tm);
+    if (p.windows > 1) {  // some sequence may have more than one segment
+        const unsigned several = static_cast<unsigned>(std::min<int64_t>({dims->sequences, p.windows, 64}));
+        ssd_varlen_kernel<true><<<ctas, kVarThreads, VarSmem::kTotal, s>>>(p, tm);
+        ssd_varlen_combine_kernel<<<dim3(static_cast<unsigned>(H) * 8, several), 256, 0, s>>>(p);
+    }
+    ssd_varlen_kernel<false><<<ctas, kVarThreads, VarSmem::kTotal, s>>>(p, tm);
     return launched();
 }
 
@@ -528,7 +543,7 @@ int ssm_ssd_varlen_fwd(const void *x, const void *dt, const float *dt_bias, int 
                        const uint8_t *has_initial, void *y, void *workspace, size_t workspace_bytes,
                        const ssm_ssd_packed_dims_t *dims, ssm_stream_t stream) {
     return ssd_varlen_impl(x, dt, dt_bias, softplus, A, B, C, D, cu_seqlens, states, slots, has_initial, y, workspace,
-                           workspace_bytes, dims, stream, 0u, kSsdFlagLimit);
+                           workspace_bytes, dims, stream, 1u, kSsdFlagLimit);
 }
 
 int ssm_debug_ssd_varlen_flag_timeout(const void *x, const void *dt, const float *dt_bias, int softplus, const float *A,

@@ -3,40 +3,44 @@
 //
 //   H_t = exp(dt_t A) H_{t-1} + dt_t x_t B_t^T,   y_t = H_t C_t + D x_t   per head
 //
-// over chunks of at most Q = 128 steps.  With cs the running sum of dt A in the
-// chunk and any reference m, exp(cs_i - cs_j) = exp(cs_i - m) exp(m - cs_j), so
-// both factors can leave the matrix C B^T and the chunk becomes
+// over chunks of Q = 128 steps.  With d_i = cs_i - cs_last (cs the running sum of
+// dt A in the chunk, T its last value) and S the state before the chunk:
 //
-//   X''_j = exp(m - cs_j) dt_j x_j,   S~ = exp(m) S   (S the state before the chunk)
-//   Y_i   = sum_{j <= i} (C_i . B_j) X''_j + C_i S~,   y_i = exp(cs_i - m) Y_i + D x_i
-//   S_new = exp(cs_last - m) (S~ + sum_j X''_j B_j^T)
+//   Yd_i  = sum_{j <= i} (C_i . B_j) exp(d_i - d_j) dt_j x_j,   Yo_i = C_i S
+//   y_i   = Yd_i + exp(d_i + T) Yo_i + D x_i
+//   S_new = exp(T) S + sum_j exp(-d_j) dt_j x_j B_j^T
 //
-// The lower triangle of C B^T is the same for every head of a group: it is
-// formed once for the two heads that a CTA walks together, and everything per
-// head is a scaling of rows.  S~ + X''^T B accumulates in tensor memory on S~
-// itself, exp(cs_last - m) joining the next chunk's exp(m).
+// C B^T is the same for every head of a group: it is formed once for the two heads
+// that a CTA walks together.  Where |d| stays below kVarRange = 80 the decays
+// factor, exp(d_i - d_j) dt_j = exp(d_i) w_j with w_j = exp(-d_j) dt_j, the same
+// w_j that scales x for the state; else they are taken element by element.  (With
+// softplus d runs one way, so the factors' product stays below e^80 even where the
+// mask drops it; without it the limit is half of that.  The
+// row factor is not left to the end, though that would save the per-head matrix:
+// the tensor core aligns a sum's products to the largest, and counts a masked zero
+// as 2^-126 times its x; with x scaled over e^110 the first rows of a chunk came
+// out wrong by their whole value, and shorter chunks made heads of strong decay
+// the longest chain.)  The state accumulates in tensor memory on exp(T) S itself.
 //
-// The factors must stay in range: m is the middle of cs over the chunk's rows,
-// and a chunk ends early where cs would span more than kVarSpan = 80, so that no
-// factor leaves [e-40, e40].  What sets the limit is the tensor core's alignment
-// of a sum's products: a zero of the triangle counts there as 2^-126 times its
-// X''_j, which for the last rows is e^40, and the first rows' true products of
-// about e^-40 must not fall more than 24 bits below that.  At a span of 80 the
-// loss is below 2^-34 of dt x; at 110 the first rows of such chunks came out
-// wrong by their whole value.  Heads whose decay passes e^-80 within 128 steps
-// pay with more chunks.
+// Roundings to bf16 are those of the tensor core's operands: C B^T with its decays
+// once, S once where it meets C (each at most the half step that y's own rounding
+// is), and exp(-d) dt x as a sum of three bf16 parts, 24 bits, where it meets B.
+// The state itself stays float32.  d is summed from the chunk's end, so the steps
+// that count most for the state have the smallest rounding.
 //
-// Roundings to bf16 are those of the tensor core's operands: the triangle of
-// C B^T once, S~ once where it meets C (each no more than a half step of y's own
-// bf16), and X'' as a sum of three bf16 parts, 24 bits, where it meets B in the
-// state, of which the first two meet the triangle.  The state itself stays
-// float32, the running sums of dt A are float64.
+// Per pair of heads and chunk: 96 KB loaded through TMA and six products of
+// 128 x 128 x 128, 3072 cycles of the tensor pipe at 8192 bf16 flops a cycle;
+// shared memory carries about 670 KB for them and their operands, 5200 cycles at
+// 128 bytes a cycle, which bounds the chunk.  One CTA per SM: a producer warp
+// issues every TMA load and MMA, a table warp walks the work list a chunk ahead
+// (running sums and factors), and sixteen epilogue warps scale, mask and store.
+// Every wait is bounded.
 //
-// Per pair of heads and chunk: 98 KB loaded through TMA and 7 products of
-// 128 x 128 x 128, 3584 cycles of the tensor pipe at 8192 bf16 flops a cycle.
-// One CTA per SM: a producer warp issues every TMA load and MMA, a table warp
-// walks the work list a chunk ahead (running sums, factors, chunk lengths), and
-// eight epilogue warps scale, mask and store.  Every wait is bounded.
+// Long sequences are cut into segments.  Chained, a segment waits for the state of
+// the one before; where that would leave SMs idle (few heads, long sequences) the
+// setup kernel chooses the two-pass schedule instead: the segments' own states
+// first, from zeros and without outputs, all at once, then the states at their
+// starts (ssd_varlen_combine_kernel), then every segment by itself.
 #pragma once
 
 #include <cuda.h>
@@ -49,20 +53,22 @@ namespace ssm {
 constexpr int kVarQ = 128;          // steps of a chunk at most
 constexpr int kVarSegment = 1024;   // tokens of a work item at least (all but a sequence's last)
 constexpr int kVarMaxWindows = 1024;
-constexpr float kVarSpan = 80.0f;
-constexpr int kVarEpilogue = 256;
+constexpr float kVarRange = 80.0f;
+constexpr int kVarEpilogue = 512;
 constexpr int kVarThreads = kVarEpilogue + 64;  // + the producer warp and the table warp
 constexpr int kVarHeads = 2;        // heads walked together
-constexpr int kVarParts = 3;        // bf16 parts of X''
+constexpr int kVarParts = 3;        // bf16 parts of exp(-d) dt x
 
 // Workspace: header (error word at 16, where ssm_scan_fwd_status reads it), the
-// work list's later segments, one flag per (window, pair), one state per
-// (window, head) for sequences of more than one segment.
+// work list's later segments, and for each of them (by the window of `segment`
+// tokens it starts in) a flag per pair, a decay and a state per head.
 struct VarWork {
-    uint32_t *queue, *error, *extras;  // item counter; error word; number of later segments
+    uint32_t *queue, *error, *extras;  // item counters of the passes (2); error word; later segments
+    uint32_t *several, *parallel;      // sequences of more than one segment; the two-pass schedule
     int2 *list;                        // [windows] (sequence, segment) of the later segments
-    uint32_t *flags;                   // [windows][pairs] segments done
-    float *carry;                      // [windows][heads][P][N]
+    uint32_t *flags;                   // [windows][pairs] the state at the segment's start is written
+    float *decay;                      // [windows][heads] of the segment before it
+    float *carry;                      // [windows][heads][P][N] the state at its start
 };
 
 struct VarMaps {
@@ -78,8 +84,8 @@ struct VarParams {
     VarWork work;
     int64_t dt_stride, y_stride;
     int32_t heads, groups, pairs;  // pairs: of all groups
-    int32_t segment, windows;
-    uint32_t flag_want_bias, spin_limit;
+    int32_t segment, windows, sms;
+    uint32_t flag_want, spin_limit;
     int softplus;
 };
 
@@ -91,19 +97,30 @@ struct VarChunk {
     int32_t stop;
     const float *src;        // the state before the item, or NULL (zeros)
     float *dst;              // where its state goes, or NULL
-    uint32_t *flag;          // hand-off: set to `segment + 1` once dst is written, or NULL
-    uint32_t flag_value;
-    float sin[2], sout[2], D[2];
+    uint32_t *flag;          // hand-off: set once dst is written, or NULL
+    float decay[2], total[2], D[2];  // exp(T), T
+    int32_t factored[2];
+};
+
+// A segment of a sequence for a pair of heads, as the table warp sees it (A, bias
+// and D: of the lane's head).
+struct VarItem {
+    bool valid, more;        // more: the sequence goes on behind it
+    int32_t h0, nh, g, seg;
+    int64_t first, stop, window;  // window: of the segment's start
+    float *state;
+    const float *src;
+    float A, bias, D;
 };
 
 struct VarSmem {
     static constexpr int kTile = 128 * 128;           // [128 rows][64] bf16, 128-byte swizzle
     static constexpr int kC = 0, kB = 2 * kTile;      // [t][n]: n < 64, n >= 64
     static constexpr int kX = 4 * kTile;              // [t][p] of each head
-    static constexpr int kXp = 6 * kTile;             // X'': parts x heads tiles
-    static constexpr int kS = kXp + kVarParts * kVarHeads * kTile;  // S~ [n][p] of each head
-    static constexpr int kTabA = kS + kVarHeads * kTile;            // exp(cs - m) [head][128]
-    static constexpr int kTabW = kTabA + kVarHeads * 512;           // exp(m - cs) dt
+    static constexpr int kXp = 6 * kTile;             // exp(-d) dt x: parts x heads tiles
+    static constexpr int kS = kXp + kVarParts * kVarHeads * kTile;  // S [n][p] of each head
+    static constexpr int kTabD = kS + kVarHeads * kTile;            // d [head][128]
+    static constexpr int kTabW = kTabD + kVarHeads * 512;           // w where the decays factor, else dt
     static constexpr int kInfo = kTabW + kVarHeads * 512;
     static constexpr int kBar = kInfo + 128;
     static constexpr int kTotal = kBar + 128;
@@ -113,13 +130,14 @@ static_assert(VarSmem::kTotal <= 227 * 1024, "shared memory of the packed SSD ke
 
 // The work list: one segment per sequence first, then the later segments of the
 // longer ones by their number, so that a segment's predecessor always stands
-// before it.  A sequence of more than one segment is longer than one, so two
-// later segments never start in the same window of `segment` tokens, nor do two
-// such sequences: a window's index names both.  One block.
+// before it.  Two later segments never start in the same window of `segment`
+// tokens (those of one sequence are `segment` apart, those of the next sequence
+// start more than that behind its start), so a window's index names one.  One block.
 __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams p) {
     __shared__ int2 at[kVarMaxWindows];
-    __shared__ uint32_t count, bad;
-    if (threadIdx.x == 0) count = 0, bad = 0;
+    __shared__ uint32_t later, several, filled, bad;
+    __shared__ int longest;
+    if (threadIdx.x == 0) later = 0, several = 0, filled = 0, bad = 0, longest = 1;
     for (int k = threadIdx.x; k < p.windows; k += blockDim.x) at[k] = make_int2(-1, 0);
     for (int k = threadIdx.x; k < p.windows * p.pairs; k += blockDim.x) p.work.flags[k] = 0;
     __syncthreads();
@@ -129,8 +147,13 @@ __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams 
             bad = 1;
             continue;
         }
-        for (int s = 1; s < (b - a + p.segment - 1) / p.segment; ++s)
-            at[(static_cast<int64_t>(a) + static_cast<int64_t>(s) * p.segment) / p.segment] = make_int2(n, s);
+        const int segs = (b - a + p.segment - 1) / p.segment;
+        for (int s = 1; s < segs; ++s) at[a / p.segment + s] = make_int2(n, s);  // the window of a + s segment
+        if (segs > 0) atomicAdd(&filled, 1u);
+        if (segs > 1) {
+            atomicAdd(&several, 1u);
+            atomicMax(&longest, segs);
+        }
     }
     __syncthreads();
     for (int k = threadIdx.x; k < p.windows; k += blockDim.x) {
@@ -140,36 +163,64 @@ __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams 
         for (int o = 0; o < p.windows; ++o)
             rank += at[o].x >= 0 && (at[o].y < v.y || (at[o].y == v.y && o < k));
         p.work.list[rank] = v;
-        atomicAdd(&count, 1u);
+        atomicAdd(&later, 1u);
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        *p.work.queue = 0;
-        *p.work.extras = count;
+        p.work.queue[0] = p.work.queue[1] = 0;
+        *p.work.extras = later;
+        *p.work.several = several;
+        // the chain of the longest sequence against the segments that each SM takes, with
+        // half as much again for the first pass and two segments for its launches
+        const int64_t items = static_cast<int64_t>(filled + later) * p.pairs;
+        *p.work.parallel = p.flag_want == 1u && 2ll * longest * p.sms > 3ll * items + 4ll * p.sms;
         *p.work.error = bad ? 4u : 0u;  // a table that does not ascend within the tokens: nothing is run
     }
 }
 
-__device__ __forceinline__ float var_exp(double d) {  // exp of a float64 argument to float32's precision
-    const float f = static_cast<float>(d);
-    const float e = expf(f);
-    return fabsf(f) <= 200.0f ? fmaf(e, static_cast<float>(d - f), e) : e;
+// The states at the segments' starts from the segments' own: S_{s+1} = exp(T_s) S_s
+// + E_s, in place.  grid: (heads x 8, sequences of more than one segment at most)
+__global__ void __launch_bounds__(256) ssd_varlen_combine_kernel(const VarParams p) {
+    if ((*p.work.error & 4u) || !*p.work.parallel) return;
+    const int h = blockIdx.x / 8;
+    const int64_t e = (blockIdx.x % 8) * 256 + threadIdx.x;  // a 16-byte vector of the state
+    for (uint32_t i = blockIdx.y; i < *p.work.several; i += gridDim.y) {
+        const int n = p.work.list[i].x;  // the second segments come first in the list
+        const int64_t begin = p.seq.cu[n], end = p.seq.cu[n + 1];
+        const int segs = static_cast<int>((end - begin + p.segment - 1) / p.segment);
+        const int slot = p.states ? packed_slot(p.seq, n) : -1;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (slot >= 0 && p.seq.has_initial && p.seq.has_initial[n])
+            s = reinterpret_cast<const float4 *>(p.states + (static_cast<int64_t>(slot) * p.heads + h) * (kSsdP * kSsdN))[e];
+#pragma unroll 4
+        for (int k = 1; k < segs; ++k) {
+            const int64_t at = (begin / p.segment + k) * p.heads + h;
+            float4 *c = reinterpret_cast<float4 *>(p.work.carry + at * (kSsdP * kSsdN)) + e;
+            const float a = p.work.decay[at];
+            const float4 v = *c;
+            s.x = fmaf(a, s.x, v.x), s.y = fmaf(a, s.y, v.y), s.z = fmaf(a, s.z, v.z), s.w = fmaf(a, s.w, v.w);
+            *c = s;
+        }
+    }
 }
 
+// SUMMARY: the first pass of the two-pass schedule, which forms the segments' own
+// states only; nothing to do when the setup kernel chose the chained schedule.
+template <bool SUMMARY>
 __global__ void __launch_bounds__(kVarThreads, 1)
     ssd_varlen_kernel(const VarParams p, const __grid_constant__ VarMaps tm) {
     extern __shared__ __align__(1024) uint8_t var_smem[];
     using S = VarSmem;
     uint8_t *sm = var_smem;
-    float *tabA = reinterpret_cast<float *>(sm + S::kTabA), *tabW = reinterpret_cast<float *>(sm + S::kTabW);
+    float *tabD = reinterpret_cast<float *>(sm + S::kTabD), *tabW = reinterpret_cast<float *>(sm + S::kTabW);
     VarChunk *info = reinterpret_cast<VarChunk *>(sm + S::kInfo);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + S::kBar);
-    uint64_t *bFull = bar, *bEmpty = bar + 1;   // tables and info written; read by everyone
-    uint64_t *bX = bar + 2, *bCB = bar + 3;     // X landed; C and B landed
-    uint64_t *mG = bar + 4, *mY = bar + 5;      // C B^T done; every product of the chunk done
-    uint64_t *bE1 = bar + 6, *bE2 = bar + 7;    // X'' and S~ written; the triangle written
-    uint64_t *bOut = bar + 8;                   // a handed-on state written
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 9);
+    uint64_t *bFull = bar, *bX = bar + 1, *bCB = bar + 2;          // tables and info written; X landed; C and B landed
+    uint64_t *mG = bar + 3, *mY = bar + 4;                         // C B^T; every product of the chunk done
+    uint64_t *bEmpty = bar + 5;                                    // info read by everyone, tables done with
+    uint64_t *bS = bar + 6, *bE1 = bar + 7, *bE2 = bar + 8;        // S; the parts of x; C B^T with its decays written
+    uint64_t *bOut = bar + 9;                                      // a handed-on state written
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 10);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t *error = p.work.error;
 
@@ -179,9 +230,11 @@ __global__ void __launch_bounds__(kVarThreads, 1)
         return;
     }
     if (*reinterpret_cast<volatile uint32_t *>(error) & 4u) return;
+    const bool parallel = *reinterpret_cast<volatile uint32_t *>(p.work.parallel) != 0;
+    if (SUMMARY && !parallel) return;
     if (tid == 0) {
-        for (int i = 0; i < 9; ++i) {
-            const uint32_t n = i == 1 ? kVarEpilogue + 1 : i >= 6 ? kVarEpilogue : 1;
+        for (int i = 0; i < 10; ++i) {
+            const uint32_t n = i == 5 ? kVarEpilogue + 1 : i > 5 ? kVarEpilogue : 1;
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar + i)), "r"(n));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -194,17 +247,18 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tbase = *reinterpret_cast<volatile uint32_t *>(tslot);
-    // TMEM columns: C B^T (128), its triangle as bf16 pairs (64), Y (128), S (128:
-    // lane n holds S[p][n] of head h in column 64 h + p)
-    const uint32_t tG = tbase, tT = tbase + 128, tY = tbase + 192, tS = tbase + 320;
+    // TMEM columns: C B^T (128; its two heads' matrices replace it, as bf16 pairs: of
+    // every 32 columns the first 16 for head 0, the others for head 1), Yd, Yo and S (128
+    // each: head h's column p in 64 h + p; lane n holds S[p][n])
+    const uint32_t tG = tbase, tYd = tbase + 128, tYo = tbase + 256, tS = tbase + 384;
     constexpr int kN = 64 * kVarHeads;
 
-    if (warp == 8) {
+    if (warp == kVarEpilogue / 32) {
         // ---- producer: one lane issues the loads and the products --------------------
         if (lane == 0) {
-            const uint32_t aC = smem_u32(sm + S::kC), aB = smem_u32(sm + S::kB), aXp = smem_u32(sm + S::kXp),
-                           aS = smem_u32(sm + S::kS);
-            uint32_t nX = 0, wX = 0, nCB = 0, wCB = 0, nG = 0, nY = 0, wY = 0;  // issued, waited for
+            const uint32_t aC = smem_u32(sm + S::kC), aB = smem_u32(sm + S::kB), aX = smem_u32(sm + S::kX),
+                           aXp = smem_u32(sm + S::kXp), aS = smem_u32(sm + S::kS);
+            uint32_t nL = 0, wL = 0, nG = 0, nY = 0, wY = 0;  // issued, waited for
             int t0 = 0, h0 = 0, nh = 0, g = 0;
             auto next = [&](uint32_t u) -> bool {  // the chunk's numbers; false: no more
                 if (!ssd_wait(bFull, u & 1u, error)) return false;
@@ -214,51 +268,50 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 ssd_arrive(bEmpty);
                 return go;
             };
-            auto load_x = [&]() {
+            auto load = [&]() {
                 mbar_arrive_expect_tx(bX, nh * S::kTile);
                 for (int i = 0; i < nh; ++i) tma_load_3d(sm + S::kX + i * S::kTile, &tm.x, 0, h0 + i, t0, bX);
-                ++nX;
-            };
-            auto load_cb = [&]() {
-                mbar_arrive_expect_tx(bCB, 4 * S::kTile);
-                tma_load_3d(sm + S::kC, &tm.C, 0, g, t0, bCB);
-                tma_load_3d(sm + S::kC + S::kTile, &tm.C, 64, g, t0, bCB);
+                mbar_arrive_expect_tx(bCB, (SUMMARY ? 2 : 4) * S::kTile);
                 tma_load_3d(sm + S::kB, &tm.B, 0, g, t0, bCB);
                 tma_load_3d(sm + S::kB + S::kTile, &tm.B, 64, g, t0, bCB);
-                ++nCB;
+                if constexpr (!SUMMARY) {
+                    tma_load_3d(sm + S::kC, &tm.C, 0, g, t0, bCB);
+                    tma_load_3d(sm + S::kC + S::kTile, &tm.C, 64, g, t0, bCB);
+                }
+                ++nL;
             };
             bool go = next(0);
-            if (go) {
-                load_x();
-                load_cb();
-            }
+            if (go) load();
             for (uint32_t u = 0; go; ++u) {
                 const uint32_t ph = u & 1u;
                 if (!ssd_wait(bCB, ph, error)) break;
-                wCB = u + 1;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                {   // C B^T
-                    constexpr uint32_t id = ssd_idesc(128, 128, 0, 0);
-                    const uint64_t dC = ssd_desc(aC, 16, 1024), dB = ssd_desc(aB, 16, 1024);
+                if constexpr (!SUMMARY) {
+                    {   // C B^T
+                        constexpr uint32_t id = ssd_idesc(128, 128, 0, 0);
+                        const uint64_t dC = ssd_desc(aC, 16, 1024), dB = ssd_desc(aB, 16, 1024);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t o = ((k / 4) * S::kTile + (k % 4) * 32) >> 4;
-                        ssd_mma(tG, dC + o, dB + o, id, k > 0);
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t o = ((k / 4) * S::kTile + (k % 4) * 32) >> 4;
+                            ssd_mma(tG, dC + o, dB + o, id, k > 0);
+                        }
+                        ssd_commit(mG);
+                        nG = u + 1;
                     }
-                    ssd_commit(mG);
-                    nG = u + 1;
-                }
-                if (!ssd_wait(bE1, ph, error)) break;
-                wX = u + 1;  // the epilogue warps read X before they arrived
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                {   // Y = C S~
-                    constexpr uint32_t id = ssd_idesc(128, kN, 0, 1);
-                    const uint64_t dC = ssd_desc(aC, 16, 1024), dS = ssd_desc(aS, S::kTile, 1024);
+                    if (!ssd_wait(bS, ph, error)) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    {   // Yo = C S
+                        constexpr uint32_t id = ssd_idesc(128, kN, 0, 1);
+                        const uint64_t dC = ssd_desc(aC, 16, 1024), dS = ssd_desc(aS, S::kTile, 1024);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        ssd_mma(tY, dC + (((k / 4) * S::kTile + (k % 4) * 32) >> 4), dS + ((2048 * k) >> 4), id, k > 0);
+                        for (int k = 0; k < 8; ++k)
+                            ssd_mma(tYo, dC + (((k / 4) * S::kTile + (k % 4) * 32) >> 4), dS + ((2048 * k) >> 4), id, k > 0);
+                    }
                 }
-                {   // S = S~ + B^T X'', the smallest part first
+                const bool parts = ssd_wait(bE1, ph, error);
+                if (parts) {  // S += B^T (exp(-d) dt x), the smallest part first
+                    wL = u + 1;  // the epilogue warps read X before they arrived
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     constexpr uint32_t id = ssd_idesc(128, kN, 1, 1);
                     const uint64_t dB = ssd_desc(aB, S::kTile, 1024);
 #pragma unroll
@@ -269,211 +322,191 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                             ssd_mma(tS, dB + ((2048 * k) >> 4), dX + ((2048 * k) >> 4), id, 1);
                     }
                 }
-                if (!ssd_wait(bE2, ph, error)) {
-                    ssd_commit(mY);  // the products above are in flight
-                    nY = u + 1;
-                    break;
-                }
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                {   // Y += triangle X'' (its first two parts)
-                    constexpr uint32_t id = ssd_idesc(128, kN, 0, 1);
+                bool decays = parts;
+                if constexpr (!SUMMARY) {
+                    decays = parts && ssd_wait(bE2, ph, error);
+                    if (decays) {  // Yd = (C B^T with its decays) x, per head
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        constexpr uint32_t id = ssd_idesc(128, 64, 0, 1);
+                        for (int i = 0; i < nh; ++i) {
+                            const uint64_t dX = ssd_desc(aX + i * S::kTile, S::kTile, 1024);
 #pragma unroll
-                    for (int part = 1; part >= 0; --part) {
-                        const uint64_t dX = ssd_desc(aXp + part * kVarHeads * S::kTile, S::kTile, 1024);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) ssd_mma_ts(tY, tT + 8 * k, dX + ((2048 * k) >> 4), id, 1);
+                            for (int k = 0; k < 8; ++k)
+                                ssd_mma_ts(tYd + 64 * i, tG + 32 * (k / 2) + 16 * i + 8 * (k % 2), dX + ((2048 * k) >> 4), id, k > 0);
+                        }
                     }
-                    ssd_commit(mY);
-                    nY = u + 1;
                 }
+                ssd_commit(mY);  // (also what was issued before a wait gave up)
+                nY = u + 1;
+                if (!decays) break;
                 go = next(u + 1);
-                if (go) load_x();  // X is free since bE1
                 if (!ssd_wait(mY, ph, error)) break;
                 wY = u + 1;
-                if (go) load_cb();
+                if (go) load();
             }
             // nothing in flight when the CTA ends
-            if (nX > wX) ssd_drain(bX, (nX - 1) & 1u, error);
-            if (nCB > wCB) ssd_drain(bCB, (nCB - 1) & 1u, error);
+            if (nL > wL) {
+                ssd_drain(bX, (nL - 1) & 1u, error);
+                ssd_drain(bCB, (nL - 1) & 1u, error);
+            }
             if (nG > 0) ssd_drain(mG, (nG - 1) & 1u, error);
             if (nY > wY) ssd_drain(mY, (nY - 1) & 1u, error);
         }
         __syncwarp();
-    } else if (warp == 9) {
-        // ---- table warp: items, chunk lengths, running sums and factors ---------------
-        const uint32_t total = (static_cast<uint32_t>(p.seq.sequences) + *reinterpret_cast<volatile uint32_t *>(p.work.extras)) *
-                               static_cast<uint32_t>(p.pairs);
+    } else if (warp == kVarEpilogue / 32 + 1) {
+        // ---- table warp: items, running sums and factors.  Half a warp per head, eight
+        // rows per lane; the next chunk's dt is on its way while this one's are formed. ----
+        const uint32_t sequences = SUMMARY ? 0u : static_cast<uint32_t>(p.seq.sequences);
+        const uint32_t total = (sequences + *reinterpret_cast<volatile uint32_t *>(p.work.extras)) * static_cast<uint32_t>(p.pairs);
         const int HG = p.heads / p.groups, pairs_per_group = p.pairs / p.groups;
+        const int hh = lane >> 4, sub = lane & 15;
         uint32_t u = 0;
-        auto pop = [&]() -> uint32_t {
-            uint32_t q = 0;
-            if (lane == 0) q = atomicAdd(p.work.queue, 1u);
-            return __shfl_sync(0xffffffffu, q, 0);
+        auto fetch = [&]() -> VarItem {  // the next item of the list that has tokens
+            VarItem it;
+            it.valid = false;
+            for (;;) {
+                uint32_t q = 0;
+                if (lane == 0) q = atomicAdd(p.work.queue + (SUMMARY ? 1 : 0), 1u);
+                q = __shfl_sync(0xffffffffu, q, 0);
+                if (q >= total) return it;
+                const uint32_t e = q / static_cast<uint32_t>(p.pairs);
+                const int pair = static_cast<int>(q % static_cast<uint32_t>(p.pairs));
+                int n = static_cast<int>(e);
+                it.seg = 0;
+                if (e >= sequences) {
+                    const int2 v = p.work.list[e - sequences];
+                    n = v.x, it.seg = SUMMARY ? v.y - 1 : v.y;  // (a later segment's start needs the one before)
+                }
+                const int64_t begin = packed_at(p.seq, n), end = packed_at(p.seq, n + 1);
+                it.first = begin + static_cast<int64_t>(it.seg) * p.segment;
+                it.stop = min(it.first + p.segment, end);
+                if (it.first >= it.stop) continue;
+                it.valid = true;
+                it.more = it.stop < end;
+                it.g = pair / pairs_per_group;
+                it.h0 = it.g * HG + (pair % pairs_per_group) * kVarHeads;
+                it.nh = min(kVarHeads, (it.g + 1) * HG - it.h0);
+                it.window = begin / p.segment + it.seg;
+                const int slot = p.states ? packed_slot(p.seq, n) : -1;
+                it.state = slot >= 0 ? p.states + (static_cast<int64_t>(slot) * p.heads + it.h0) * (kSsdP * kSsdN) : nullptr;
+                it.src = it.state && p.seq.has_initial && p.seq.has_initial[n] ? it.state : nullptr;
+                if (it.seg > 0) it.src = p.work.carry + (it.window * p.heads + it.h0) * (kSsdP * kSsdN);
+                if (SUMMARY) it.src = nullptr;
+                const int h = it.h0 + (hh < it.nh ? hh : 0);
+                it.A = p.A[h];
+                it.bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
+                it.D = p.D ? p.D[h] : 0.0f;
+                return it;
+            }
+        };
+        uint16_t raw[8];
+        auto load_dt = [&](const VarItem &it, int64_t t) {
+            const uint16_t *src = static_cast<const uint16_t *>(p.dt) + it.h0 + hh;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int64_t r = t + 8 * sub + k;
+                raw[k] = r < it.stop && hh < it.nh ? __ldg(src + r * p.dt_stride) : static_cast<uint16_t>(0);
+            }
         };
         auto ready = [&]() -> bool {  // everyone has read the chunk before
             const bool ok = u == 0 || ssd_wait(bEmpty, (u - 1) & 1u, error);
             return __all_sync(0xffffffffu, ok);
         };
         bool ok = true;
-        uint32_t q = pop();
-        while (ok && q < total) {
-            const uint32_t nextq = pop();
-            const uint32_t e = q / static_cast<uint32_t>(p.pairs);
-            const int pair = static_cast<int>(q % static_cast<uint32_t>(p.pairs));
-            q = nextq;
-            int n = static_cast<int>(e), seg = 0;
-            if (e >= static_cast<uint32_t>(p.seq.sequences)) {
-                const int2 v = p.work.list[e - p.seq.sequences];
-                n = v.x, seg = v.y;
-            }
-            const int64_t begin = packed_at(p.seq, n), end = packed_at(p.seq, n + 1);
-            const int64_t first = begin + static_cast<int64_t>(seg) * p.segment, stop = min(first + p.segment, end);
-            if (first >= stop) continue;
-            const int g = pair / pairs_per_group, h0 = g * HG + (pair % pairs_per_group) * kVarHeads;
-            const int nh = min(kVarHeads, (g + 1) * HG - h0);
-            const int slot = p.states ? packed_slot(p.seq, n) : -1;
-            const int64_t window = begin / p.segment;
-            float *carry = p.work.carry + (window * p.heads + h0) * (kSsdP * kSsdN);
-            float *state = slot >= 0 ? p.states + (static_cast<int64_t>(slot) * p.heads + h0) * (kSsdP * kSsdN) : nullptr;
-            uint32_t *flag = p.work.flags + window * p.pairs + pair;
-            const float *src = nullptr;
-            if (seg > 0) {
-                bool got = false;  // the segment before, walked by a CTA that took it earlier
-                if (lane == 0) {
-                    const uint32_t want = static_cast<uint32_t>(seg) + p.flag_want_bias;
-                    for (uint32_t i = 0; i < p.spin_limit; ++i) {
-                        if (ld_acquire(flag) >= want) {
-                            got = true;
-                            break;
-                        }
-                        if ((i & 255u) == 255u && *reinterpret_cast<volatile uint32_t *>(error) != 0) break;
-                        __nanosleep(64);
-                    }
-                    if (!got) atomicOr(error, 2u);
+        VarItem it = fetch();
+        if (it.valid) load_dt(it, it.first);
+        while (ok && it.valid) {
+            const VarItem nxt = fetch();
+            float item_total = 0.0f;
+            for (int64_t t = it.first; t < it.stop; t += kVarQ) {
+                const int rows = static_cast<int>(min(static_cast<int64_t>(kVarQ), it.stop - t));
+                const bool last_chunk = t + rows >= it.stop;
+                float dt[8], d[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    dt[k] = __uint_as_float(static_cast<uint32_t>(raw[k]) << 16) + it.bias;
+                    if (p.softplus) dt[k] = softplus_accurate(dt[k]);
+                    if (8 * sub + k >= rows || hh >= it.nh) dt[k] = 0.0f;
                 }
-                if (!__shfl_sync(0xffffffffu, static_cast<int>(got), 0)) {
-                    ok = false;
-                    break;
+                if (!last_chunk) load_dt(it, t + rows);
+                else if (nxt.valid) load_dt(nxt, nxt.first);
+                // d_j = minus the sum of the later rows' dt A
+                float after = 0.0f;
+#pragma unroll
+                for (int k = 7; k >= 0; --k) {
+                    d[k] = after;
+                    after -= dt[k] * it.A;
                 }
-                src = carry;
-            } else if (state && p.seq.has_initial && p.seq.has_initial[n]) {
-                src = state;
-            }
-            const bool more = stop < end;
-            float A[kVarHeads], bias[kVarHeads], D[kVarHeads];
+                float sum = after;
 #pragma unroll
-            for (int i = 0; i < kVarHeads; ++i) {
-                const int h = h0 + (i < nh ? i : 0);
-                A[i] = p.A[h];
-                bias[i] = p.dt_bias ? p.dt_bias[h] : 0.0f;
-                D[i] = p.D ? p.D[h] : 0.0f;
-            }
-            double tail[kVarHeads] = {};  // what the state in tensor memory still lacks, as an exponent
-            for (int64_t t = first; t < stop;) {
-                const int avail = static_cast<int>(min(static_cast<int64_t>(kVarQ), stop - t));
-                float dt[kVarHeads][4];
-                double cs[kVarHeads][4];
-                float lo[kVarHeads][4], hi[kVarHeads][4];
-                int rows = avail;
+                for (int o = 1; o < 16; o <<= 1) {
+                    const float v = __shfl_down_sync(0xffffffffu, sum, o, 16);
+                    if (sub + o < 16) sum += v;
+                }
+                const float T = -__shfl_sync(0xffffffffu, sum, 0, 16);
+                float later = __shfl_down_sync(0xffffffffu, sum, 1, 16);
+                if (sub == 15) later = 0.0f;
+                float most = 0.0f, w[8];
 #pragma unroll
-                for (int i = 0; i < kVarHeads; ++i) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = 4 * lane + k;
-                        dt[i][k] = 0.0f;
-                        if (r < avail && i < nh)
-                            dt[i][k] = Act<bf16raw>::load(p.dt, (t + r) * p.dt_stride + h0 + i) + bias[i];
-                    }
+                for (int k = 0; k < 8; ++k) {
+                    d[k] += later;
+                    most = fmaxf(most, fabsf(d[k]));
+                    w[k] = expf(-d[k]) * dt[k];
                 }
 #pragma unroll
-                for (int i = 0; i < kVarHeads; ++i) {
-                    double sum = 0.0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = 4 * lane + k;
-                        if (r < avail && i < nh && p.softplus) dt[i][k] = softplus_accurate(dt[i][k]);
-                        sum += static_cast<double>(dt[i][k]) * A[i];
-                        cs[i][k] = sum;
-                    }
-                    double up = sum;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const double v = __shfl_up_sync(0xffffffffu, up, o);
-                        if (lane >= o) up += v;
-                    }
-                    up -= sum;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) cs[i][k] += up;
-                    // running least and largest of cs, relative to the first row's
-                    const double c0 = __shfl_sync(0xffffffffu, cs[i][0], 0);
-                    float l = 0.0f, h = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float v = static_cast<float>(cs[i][k] - c0);
-                        l = fminf(l, v), h = fmaxf(h, v);
-                        lo[i][k] = l, hi[i][k] = h;
-                    }
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const float vl = __shfl_up_sync(0xffffffffu, l, o), vh = __shfl_up_sync(0xffffffffu, h, o);
-                        if (lane >= o) l = fminf(l, vl), h = fmaxf(h, vh);
-                    }
-                    l = __shfl_up_sync(0xffffffffu, l, 1), h = __shfl_up_sync(0xffffffffu, h, 1);
-                    if (lane == 0) l = 0.0f, h = 0.0f;
-                    int out = kVarQ;
-#pragma unroll
-                    for (int k = 3; k >= 0; --k) {
-                        lo[i][k] = fminf(lo[i][k], l), hi[i][k] = fmaxf(hi[i][k], h);
-                        if (hi[i][k] - lo[i][k] > kVarSpan) out = 4 * lane + k;
-                    }
-                    rows = min(rows, static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(out))));
-                }
-                rows = max(rows, 1);
-                if (!ready()) {
-                    ok = false;
-                    break;
-                }
-                const int rl = (rows - 1) >> 2, rk = (rows - 1) & 3;
-#pragma unroll
-                for (int i = 0; i < kVarHeads; ++i) {
-                    const double c0 = __shfl_sync(0xffffffffu, cs[i][0], 0);
-                    double last = cs[i][0];
-                    float l = lo[i][0], h = hi[i][0];
-#pragma unroll
-                    for (int k = 1; k < 4; ++k)
-                        if (rk == k) last = cs[i][k], l = lo[i][k], h = hi[i][k];
-                    last = __shfl_sync(0xffffffffu, last, rl);
-                    l = __shfl_sync(0xffffffffu, l, rl), h = __shfl_sync(0xffffffffu, h, rl);
-                    const double m = c0 + 0.5 * (static_cast<double>(l) + h);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = 4 * lane + k;
-                        const bool in = r < rows && i < nh;
-                        tabA[i * kVarQ + r] = in ? var_exp(cs[i][k] - m) : 0.0f;
-                        tabW[i * kVarQ + r] = in ? var_exp(m - cs[i][k]) * dt[i][k] : 0.0f;
-                    }
+                for (int o = 8; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                const bool factored = most <= (p.softplus ? kVarRange : 0.5f * kVarRange);
+                item_total += T;
+                if (!SUMMARY && !parallel && t == it.first && it.seg > 0) {  // the segment before, taken earlier by some CTA
+                    bool got = false;
                     if (lane == 0) {
-                        info->sin[i] = var_exp(m + tail[i]);
-                        info->sout[i] = var_exp(last - m);
-                        info->D[i] = D[i];
+                        const uint32_t *flag = p.work.flags + it.window * p.pairs + it.g * pairs_per_group +
+                                               (it.h0 - it.g * HG) / kVarHeads;
+                        for (uint32_t i = 0; i < p.spin_limit; ++i) {
+                            if (ld_acquire(flag) >= p.flag_want) {
+                                got = true;
+                                break;
+                            }
+                            if ((i & 255u) == 255u && *reinterpret_cast<volatile uint32_t *>(error) != 0) break;
+                            __nanosleep(64);
+                        }
+                        if (!got) atomicOr(error, 2u);
                     }
-                    tail[i] = last - m;
+                    ok = __shfl_sync(0xffffffffu, static_cast<int>(got), 0) != 0;
+                }
+                if (!ok || !ready()) {
+                    ok = false;
+                    break;
+                }
+                float4 *pd = reinterpret_cast<float4 *>(tabD + hh * kVarQ + 8 * sub), *pw = reinterpret_cast<float4 *>(tabW + hh * kVarQ + 8 * sub);
+                pd[0] = make_float4(d[0], d[1], d[2], d[3]), pd[1] = make_float4(d[4], d[5], d[6], d[7]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (!factored) w[k] = dt[k];
+                pw[0] = make_float4(w[0], w[1], w[2], w[3]), pw[1] = make_float4(w[4], w[5], w[6], w[7]);
+                if (sub == 0) {
+                    info->decay[hh] = expf(T), info->total[hh] = T, info->D[hh] = it.D;
+                    info->factored[hh] = factored;
+                    if (SUMMARY && last_chunk && hh < it.nh) p.work.decay[(it.window + 1) * p.heads + it.h0 + hh] = expf(item_total);
                 }
                 if (lane == 0) {
                     info->t0 = static_cast<int>(t), info->rows = rows;
-                    info->h0 = h0, info->nh = nh, info->g = g;
-                    info->first = t == first, info->last = t + rows >= stop;
+                    info->h0 = it.h0, info->nh = it.nh, info->g = it.g;
+                    info->first = t == it.first, info->last = last_chunk;
                     info->stop = 0;
-                    info->src = src;
-                    info->dst = more ? carry : state;
-                    info->flag = more ? flag : nullptr;
-                    info->flag_value = static_cast<uint32_t>(seg) + 1u;
+                    info->src = it.src;
+                    const bool hand = SUMMARY || (it.more && !parallel);
+                    info->dst = hand ? p.work.carry + ((it.window + 1) * p.heads + it.h0) * (kSsdP * kSsdN)
+                                     : it.more ? nullptr : it.state;
+                    info->flag = hand && !SUMMARY ? p.work.flags + (it.window + 1) * p.pairs + it.g * pairs_per_group +
+                                                        (it.h0 - it.g * HG) / kVarHeads
+                                                  : nullptr;
                 }
                 __syncwarp();
                 if (lane == 0) ssd_arrive(bFull);
                 ++u;
-                t += rows;
             }
+            it = nxt;
         }
         if (ready() && lane == 0) {
             info->stop = 1;
@@ -481,64 +514,79 @@ __global__ void __launch_bounds__(kVarThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---- epilogue warps: thread (row, half) has row 32 quad + lane of every
-        // [128][..] tile (its TMEM lane) and the columns of head `half` --------------------
-        const int quad = warp & 3, head = warp >> 2, row = quad * 32 + lane;
+        // ---- epilogue warps: a thread has row 32 quad + lane of every [128][..] tile (its
+        // TMEM lane) and 32 of head `head`'s 64 columns ------------------------------------
+        const int quad = warp & 3, head = (warp >> 2) & 1, c0 = 32 * (warp >> 3), row = quad * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t tSh = tS + lane_off + 64 * head, tYh = tY + lane_off + 64 * head;
+        const uint32_t col = lane_off + 64 * head + c0;
         uint8_t *xraw = sm + S::kX + head * S::kTile, *stile = sm + S::kS + head * S::kTile;
         uint32_t handed = 0;  // states handed on by this CTA so far
+        bool ok = true;
         for (uint32_t u = 0;; ++u) {
             const uint32_t ph = u & 1u;
-            if (!__all_sync(0xffffffffu, ssd_wait(bFull, ph, error))) break;
+            ok = __all_sync(0xffffffffu, ssd_wait(bFull, ph, error));
+            if (!ok || info->stop) break;
             const VarChunk &c = *info;
-            if (c.stop) break;
             const int t0 = c.t0, rows = c.rows, h = c.h0 + head;
             const bool first = c.first, last = c.last, live = head < c.nh;
             const float *src = c.src;
             float *dst = c.dst;
             uint32_t *flag = c.flag;
-            const uint32_t flag_value = c.flag_value;
-            const float sin = c.sin[head], sout = c.sout[head], D = c.D[head];
-            const float a = tabA[head * kVarQ + row], w = tabW[head * kVarQ + row];
-            ssd_arrive(bEmpty);
+            const float decay = c.decay[head], D = c.D[head];
+            const int fac0 = c.factored[0], fac1 = c.factored[1];
+            const float di0 = tabD[row], di1 = tabD[kVarQ + row];
+            const float di = head ? di1 : di0;
+            const float eo = expf(di + c.total[head]);  // of Yo's row
+            float w = tabW[head * kVarQ + row];
+            if (!(head ? fac1 : fac0)) w *= expf(-di);
+            if constexpr (SUMMARY) ssd_arrive(bEmpty);
 
-            // S~ = exp(m) S: float32 to tensor memory, bf16 to its operand tile [n][p]
+            // S as bf16 to its operand tile [n][p]; exp(T) S, float32, to tensor memory
 #pragma unroll
-            for (int q0 = 0; q0 < 64; q0 += 16) {
+            for (int q0 = 0; q0 < 32; q0 += 16) {
                 float v[16];
                 if (!first) {
-                    ssd_ld16(tSh + q0, v);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] *= sin;
+                    ssd_ld16(tS + col + q0, v);
                 } else if (src && live) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        v[e] = sin * __ldcg(src + (head * kSsdP + q0 + e) * kSsdN + row);
+                    for (int e = 0; e < 16; ++e) v[e] = __ldcg(src + (head * kSsdP + c0 + q0 + e) * kSsdN + row);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] = 0.0f;
                 }
                 uint32_t r[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(v[e]);
-                ssd_st16(tSh + q0, r);
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(decay * v[e]);
+                ssd_st16(tS + col + q0, r);
+                if constexpr (!SUMMARY) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    *reinterpret_cast<uint4 *>(stile + ssd_sw128(row, q0 + 8 * k)) =
-                        make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                                   pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<uint4 *>(stile + ssd_sw128(row, c0 + q0 + 8 * k)) =
+                            make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                                       pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+                }
             }
-            // X'' = exp(m - cs) dt x as three bf16 parts; rows past the chunk's end are
-            // zeros whatever they hold (another sequence's values, or none)
-            if (!__all_sync(0xffffffffu, ssd_wait(bX, ph, error))) break;
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            if constexpr (!SUMMARY) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                ssd_arrive(bS);
+            }
+
+            // exp(-d) dt x as three bf16 parts; rows past the chunk's end are zeros whatever
+            // they hold (another sequence's values, or none)
+            ok = __all_sync(0xffffffffu, ssd_wait(bX, ph, error));
+            if (!ok) break;
             const bool in = row < rows && live;
-            uint32_t xr[32];  // the raw row, kept for D x
+            uint32_t xr[16];  // the raw row, kept for D x
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t o = ssd_sw128(row, 8 * k);
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t o = ssd_sw128(row, c0 + 8 * k);
                 uint4 xv = *reinterpret_cast<const uint4 *>(xraw + o);
-                if (!in) xv = make_uint4(0, 0, 0, 0);
+                if (!in) {
+                    xv = make_uint4(0, 0, 0, 0);
+                    if (!SUMMARY && live) *reinterpret_cast<uint4 *>(xraw + o) = xv;  // Yd's operand too
+                }
                 xr[4 * k] = xv.x, xr[4 * k + 1] = xv.y, xr[4 * k + 2] = xv.z, xr[4 * k + 3] = xv.w;
                 uint32_t part[kVarParts][4];
 #pragma unroll
@@ -557,89 +605,125 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                     *reinterpret_cast<uint4 *>(sm + S::kXp + (i * kVarHeads + head) * S::kTile + o) =
                         make_uint4(part[i][0], part[i][1], part[i][2], part[i][3]);
             }
-            // B's rows past the end meet X''s zeros, but a NaN there would not vanish
+            // B's rows past the end meet zeros, but a NaN there would not vanish
             if (rows < kVarQ) {
-                if (!__all_sync(0xffffffffu, ssd_wait(bCB, ph, error))) break;
+                ok = __all_sync(0xffffffffu, ssd_wait(bCB, ph, error));
+                if (!ok) break;
                 if (row >= rows) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<uint4 *>(sm + S::kB + head * S::kTile + ssd_sw128(row, 8 * k)) = make_uint4(0, 0, 0, 0);
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4 *>(sm + S::kB + head * S::kTile + ssd_sw128(row, c0 + 8 * k)) = make_uint4(0, 0, 0, 0);
                 }
             }
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             ssd_arrive(bE1);
 
-            // the lower triangle of C B^T as bf16, columns 64 head .. 64 head + 63 of it
-            if (!__all_sync(0xffffffffu, ssd_wait(mG, ph, error))) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if constexpr (!SUMMARY) {
+                // C B^T with the decays of both heads, as bf16, over its own columns: this
+                // thread's 32 columns j of its row i
+                ok = __all_sync(0xffffffffu, ssd_wait(mG, ph, error));
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const int j0 = 64 * head + c0;
+                float v[32];
+                {
+                    float v0[16], v1[16];
+                    ssd_ld16(tG + lane_off + j0, v0);
+                    ssd_ld16(tG + lane_off + j0 + 16, v1);
 #pragma unroll
-            for (int j0 = 0; j0 < 64; j0 += 32) {
-                float v0[16], v1[16];
-                ssd_ld16(tG + lane_off + 64 * head + j0, v0);
-                ssd_ld16(tG + lane_off + 64 * head + j0 + 16, v1);
-                uint32_t r[16];
-                const int j = 64 * head + j0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    r[e] = pack_bf16x2(j + 2 * e <= row ? v0[2 * e] : 0.0f, j + 2 * e + 1 <= row ? v0[2 * e + 1] : 0.0f);
-                    r[8 + e] = pack_bf16x2(j + 16 + 2 * e <= row ? v1[2 * e] : 0.0f,
-                                           j + 17 + 2 * e <= row ? v1[2 * e + 1] : 0.0f);
+                    for (int e = 0; e < 16; ++e) {  // the causal mask, by selection: a zero whatever the later rows hold
+                        v[e] = j0 + e <= row ? v0[e] : 0.0f;
+                        v[16 + e] = j0 + 16 + e <= row ? v1[e] : 0.0f;
+                    }
                 }
-                ssd_st16(tT + lane_off + 32 * head + j0 / 2, r);
+#pragma unroll
+                for (int i = 0; i < kVarHeads; ++i) {
+                    const float4 *wj = reinterpret_cast<const float4 *>(tabW + i * kVarQ + j0);
+                    const float dr = i ? di1 : di0;
+                    uint32_t r[16];
+                    if (i ? fac1 : fac0) {
+                        const float e = expf(dr);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 f = wj[k];
+                            r[2 * k] = pack_bf16x2(v[4 * k] * (e * f.x), v[4 * k + 1] * (e * f.y));
+                            r[2 * k + 1] = pack_bf16x2(v[4 * k + 2] * (e * f.z), v[4 * k + 3] * (e * f.w));
+                        }
+                    } else {
+                        // later rows (d smaller) would give factors above one, up to infinity:
+                        // their products are zeros by the mask, so the factor is capped there
+                        const float4 *dj = reinterpret_cast<const float4 *>(tabD + i * kVarQ + j0);
+                        auto factor = [&](float dc, float dtc, int j) {
+                            return j <= row ? ex2_approx((dr - dc) * kLog2e) * dtc : 0.0f;
+                        };
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 f = wj[k], dd = dj[k];
+                            const int j = j0 + 4 * k;
+                            r[2 * k] = pack_bf16x2(v[4 * k] * factor(dd.x, f.x, j), v[4 * k + 1] * factor(dd.y, f.y, j + 1));
+                            r[2 * k + 1] = pack_bf16x2(v[4 * k + 2] * factor(dd.z, f.z, j + 2), v[4 * k + 3] * factor(dd.w, f.w, j + 3));
+                        }
+                    }
+                    ssd_st16(tG + lane_off + j0 + 16 * i, r);
+                }
+                ssd_arrive(bEmpty);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                ssd_arrive(bE2);
             }
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            ssd_arrive(bE2);
 
-            if (!__all_sync(0xffffffffu, ssd_wait(mY, ph, error))) break;
+            ok = __all_sync(0xffffffffu, ssd_wait(mY, ph, error));
+            if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            // y = exp(cs - m) Y + D x, through this warp's rows of the first X'' tile (read
-            // by the products that are done) so that each store writes whole lines
-            uint8_t *stage = sm + S::kXp + head * S::kTile;
+            if constexpr (!SUMMARY) {
+                // y = Yd + exp(d + T) Yo + D x, through this warp's part of the S tile (read by
+                // the products that are done) so that each store writes whole sectors
 #pragma unroll
-            for (int q0 = 0; q0 < 64; q0 += 16) {
-                float v[16];
-                ssd_ld16(tYh + q0, v);
-                uint32_t pk[8];
+                for (int q0 = 0; q0 < 32; q0 += 16) {
+                    float yd[16], yo[16];
+                    ssd_ld16(tYo + col + q0, yo);
+                    ssd_ld16(tYd + col + q0, yd);
+                    uint32_t pk[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t x = xr[q0 / 2 + e];
-                    pk[e] = pack_bf16x2(fmaf(a, v[2 * e], D * __uint_as_float(x << 16)),
-                                        fmaf(a, v[2 * e + 1], D * __uint_as_float(x & 0xffff0000u)));
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t x = xr[q0 / 2 + e];
+                        pk[e] = pack_bf16x2(fmaf(eo, yo[2 * e], fmaf(D, __uint_as_float(x << 16), yd[2 * e])),
+                                            fmaf(eo, yo[2 * e + 1], fmaf(D, __uint_as_float(x & 0xffff0000u), yd[2 * e + 1])));
+                    }
+                    *reinterpret_cast<uint4 *>(stile + ssd_sw128(row, c0 + q0)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    *reinterpret_cast<uint4 *>(stile + ssd_sw128(row, c0 + q0 + 8)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
                 }
-                *reinterpret_cast<uint4 *>(stage + ssd_sw128(row, q0)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                *reinterpret_cast<uint4 *>(stage + ssd_sw128(row, q0 + 8)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-            }
-            __syncwarp();
-            if (live) {
-                uint16_t *yg = static_cast<uint16_t *>(p.y) + static_cast<int64_t>(t0) * p.y_stride + h * kSsdP;
+                __syncwarp();
+                if (live) {
+                    uint16_t *yg = static_cast<uint16_t *>(p.y) + static_cast<int64_t>(t0) * p.y_stride + h * kSsdP;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int r = quad * 32 + 4 * k + (lane >> 3);
-                    if (r < rows)
-                        *reinterpret_cast<uint4 *>(yg + r * p.y_stride + 8 * (lane & 7)) =
-                            *reinterpret_cast<const uint4 *>(stage + ssd_sw128(r, 8 * (lane & 7)));
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = quad * 32 + 8 * k + (lane >> 2), cc = c0 + 8 * (lane & 3);
+                        if (r < rows)
+                            *reinterpret_cast<uint4 *>(yg + r * p.y_stride + cc) =
+                                *reinterpret_cast<const uint4 *>(stile + ssd_sw128(r, cc));
+                    }
                 }
+                __syncwarp();  // the tile is S again in the next chunk
             }
-            __syncwarp();  // the rows are X'' again in the next chunk
+            // the state after an item, and its hand-off once every thread's part is written
             if (last && dst) {
                 if (live) {
 #pragma unroll
-                    for (int q0 = 0; q0 < 64; q0 += 16) {
+                    for (int q0 = 0; q0 < 32; q0 += 16) {
                         float v[16];
-                        ssd_ld16(tSh + q0, v);
+                        ssd_ld16(tS + col + q0, v);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) dst[(head * kSsdP + q0 + e) * kSsdN + row] = sout * v[e];
+                        for (int e = 0; e < 16; ++e) dst[(head * kSsdP + c0 + q0 + e) * kSsdN + row] = v[e];
                     }
                 }
-                if (flag) {  // hand the state on once every thread's part of it is written
+                if (flag) {
                     __threadfence();
                     ssd_arrive(bOut);
                     if (tid == 0 && ssd_wait(bOut, handed & 1u, error)) {
                         __threadfence();
-                        st_release(flag, flag_value);
+                        st_release(flag, 1u);
                     }
                     ++handed;
                     __syncwarp();
