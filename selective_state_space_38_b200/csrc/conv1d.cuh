@@ -32,91 +32,169 @@ struct Conv1dParams {
     float *dw, *dbias;    // [dim][K], [dim] (dbias may be NULL)
     Packed seq;
     int64_t dim, x_stride, y_stride, dy_stride, dx_stride;
-    int64_t tile;         // rows of a tile of the gradient kernel
+    int64_t tile;         // rows of a tile
     uint32_t cblocks;     // channel blocks: block i takes channel block i % cblocks of tile (or row) i / cblocks
     int silu;
 };
 
 constexpr int kConvThreads = 128;
-constexpr int kConvTile = 32;   // rows of a tile of the forward kernel
 constexpr int kConvBatch = 8;   // rows loaded ahead
+constexpr int kConvBwdBatch = 4;
 
-// The K - 1 inputs before row t of sequence n (which starts at `start`): h[d]
-// is the row d + 1 back.  Rows before the start come from the window when the
-// sequence goes on from one.
+// The sequences of a block's tile.  All its rows are walked by every thread of the
+// block in step, so the current sequence is the block's; the first 32 from the
+// tile's start wait in shared memory, since each would cost dependent loads.
+struct ConvWalk {
+    int n;               // the current sequence (`sequences`: none any more)
+    int64_t start, end;  // its rows
+    int slot;            // the window it goes on from, or -1
+    const int64_t *ends;
+    const int *slots;
+    int base;
+
+    __device__ __forceinline__ static void stage(const Conv1dParams &p, int base, int64_t *ends, int *slots) {
+        const int i = threadIdx.x;
+        if (i < 32) {
+            const int n = base + i;
+            const bool in = n < p.seq.sequences;
+            ends[i] = in ? packed_at(p.seq, n + 1) : 0;
+            slots[i] = in && p.windows && p.seq.has_initial && p.seq.has_initial[n] ? packed_slot(p.seq, n) : -1;
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ void enter(const Conv1dParams &p) {  // sequence n
+        const int i = n - base;
+        if (i < 32) {
+            start = i > 0 ? ends[i - 1] : packed_at(p.seq, n);
+            end = ends[i];
+            slot = slots[i];
+        } else {
+            start = packed_at(p.seq, n);
+            end = packed_at(p.seq, n + 1);
+            slot = p.windows && p.seq.has_initial && p.seq.has_initial[n] ? packed_slot(p.seq, n) : -1;
+        }
+    }
+    // on to the sequence that row t is in; false: behind the last one
+    __device__ __forceinline__ bool to(const Conv1dParams &p, int64_t t) {
+        do {
+            if (n + 1 >= p.seq.sequences) {
+                n = p.seq.sequences;
+                return false;
+            }
+            ++n;
+            enter(p);
+        } while (t >= end);
+        return true;
+    }
+};
+
+// A thread's V channels: taps, bias and the last K - 1 inputs (h[d]: d + 1 rows back).
 template <typename T, int V, int K>
-__device__ __forceinline__ void conv_history(const Conv1dParams &p, int n, int64_t start, int64_t t, int64_t c,
-                                             float (&h)[K > 1 ? K - 1 : 1][V]) {
-    if constexpr (K > 1) {
-        using R = Row<T, V>;
-        const int64_t pos = t > start ? t - start : 0;
-        int slot = -1;
-        if (pos < K - 1 && p.windows && p.seq.has_initial && p.seq.has_initial[n]) slot = packed_slot(p.seq, n);
+struct ConvChannels {
+    using R = Row<T, V>;
+    static constexpr int kL = R::kL, kN = R::kN, kH = K > 1 ? K - 1 : 1;
+    Lanes<kL> w[K][kN], b[kN], h[kH][kN];
+
+    __device__ __forceinline__ void taps(const Conv1dParams &p, int64_t c) {
+        float f[K * V], g[V];
+        load_params<K * V, (V > 1)>(p.w + c * K, f);
+        if (p.bias) {
+            load_params<V, (V > 1)>(p.bias + c, g);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) g[e] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) w[k][i] = Lanes<kL>::of(f[i * kL * K + k], f[(i * kL + kL - 1) * K + k]);
+            b[i] = Lanes<kL>::of(g[i * kL], g[i * kL + kL - 1]);
+        }
+    }
+    // The inputs before row t of the current sequence: its rows, before its first the
+    // window it goes on from, else zeros.
+    __device__ __forceinline__ void history(const Conv1dParams &p, const ConvWalk &q, int64_t t, int64_t c) {
+        const int64_t pos = t > q.start ? t - q.start : 0;
 #pragma unroll
         for (int d = 0; d < K - 1; ++d) {
             typename R::Raw r = R::zero_raw();
             if (pos - d - 1 >= 0) r = R::load_raw(p.x, (t - d - 1) * p.x_stride + c);
-            else if (slot >= 0) r = R::load_raw(p.windows, (static_cast<int64_t>(slot) * (K - 1) + (K - 1 + pos - d - 1)) * p.dim + c);
+            else if (q.slot >= 0) r = R::load_raw(p.windows, (static_cast<int64_t>(q.slot) * (K - 1) + (K - 1 + pos - d - 1)) * p.dim + c);
 #pragma unroll
-            for (int e = 0; e < V; ++e) h[d][e] = R::get(r, e);
+            for (int i = 0; i < kN; ++i) h[d][i] = R::pair(r, i);
         }
     }
-}
-
-template <typename T, int V, int K>
-__device__ __forceinline__ void conv_taps(const Conv1dParams &p, int64_t c, float (&w)[K][V], float (&b)[V]) {
+    // u of one row; the history moves on
+    __device__ __forceinline__ void row(const Lanes<kL> (&x)[kN], Lanes<kL> (&u)[kN]) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
+        for (int i = 0; i < kN; ++i) {
+            u[i] = Lanes<kL>::fma(w[K - 1][i], x[i], b[i]);
 #pragma unroll
-        for (int k = 0; k < K; ++k) w[k][e] = __ldg(p.w + (c + e) * K + k);
-        b[e] = p.bias ? __ldg(p.bias + c + e) : 0.0f;
+            for (int d = 0; d < K - 1; ++d) u[i] = Lanes<kL>::fma(w[K - 2 - d][i], h[d][i], u[i]);
+#pragma unroll
+            for (int d = K - 2; d > 0; --d) h[d][i] = h[d - 1][i];
+            if constexpr (K > 1) h[0][i] = x[i];
+        }
     }
-}
+};
 
 // grid: row tiles x channel blocks, the channel blocks of a tile next to each other
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(kConvThreads) conv1d_fwd_kernel(const Conv1dParams p) {
     using R = Row<T, V>;
     constexpr bool kAccurate = Act<T>::kBytes == 4;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x / p.cblocks) * kConvTile;
-    const int64_t t1 = min(t0 + kConvTile, p.seq.tokens);
-    int n = packed_find(p.seq, t0);  // the whole block walks the same rows: n and its bounds are uniform
-    if (n >= p.seq.sequences) return;
+    constexpr int kL = R::kL, kN = R::kN;
+    __shared__ int64_t ends[32];
+    __shared__ int slots[32];
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x / p.cblocks) * p.tile;
+    const int64_t t1 = min(t0 + p.tile, p.seq.tokens);
+    ConvWalk q;
+    q.n = q.base = packed_find(p.seq, t0);
+    q.ends = ends, q.slots = slots;
+    if (q.n >= p.seq.sequences) return;
+    ConvWalk::stage(p, q.base, ends, slots);
     const int64_t c = (static_cast<int64_t>(blockIdx.x % p.cblocks) * kConvThreads + threadIdx.x) * V;
     if (c >= p.dim) return;
-    float w[K][V], b[V], h[K > 1 ? K - 1 : 1][V];
-    conv_taps<T, V, K>(p, c, w, b);
-    int64_t start = packed_at(p.seq, n), end = packed_at(p.seq, n + 1);
-    conv_history<T, V, K>(p, n, start, t0, c, h);
-    for (int64_t t = t0; t < t1; t += kConvBatch) {
-        typename R::Raw raw[kConvBatch];
+    ConvChannels<T, V, K> ch;
+    typename R::Raw raw[kConvBatch];
+    auto load = [&](int64_t t) {
 #pragma unroll
         for (int i = 0; i < kConvBatch; ++i)
-            raw[i] = t + i < t1 ? R::load_raw(p.x, (t + i) * p.x_stride + c) : R::zero_raw();
+            if (t + i < t1) raw[i] = R::load_raw(p.x, (t + i) * p.x_stride + c);
+    };
+    load(t0);
+    q.enter(p);
+    ch.taps(p, c);
+    ch.history(p, q, t0, c);
+    auto row = [&](int64_t t, const typename R::Raw &r) {
+        Lanes<kL> x[kN], u[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) x[i] = R::pair(r, i);
+        ch.row(x, u);
+        if (p.silu) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) u[i] = u[i] * sigmoid_lanes<kAccurate, kL>(u[i]);
+        }
+        R::store(p.y, t * p.y_stride + c, u);
+    };
+    for (int64_t t = t0; t < t1; t += kConvBatch) {
+        typename R::Raw now[kConvBatch];
+#pragma unroll
+        for (int i = 0; i < kConvBatch; ++i) now[i] = raw[i];
+        load(t + kConvBatch);
+        if (t + kConvBatch <= min(t1, q.end)) {  // rows of one sequence: the history's moves are renamings
+#pragma unroll
+            for (int i = 0; i < kConvBatch; ++i) row(t + i, now[i]);
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < kConvBatch; ++i) {
             if (t + i >= t1) break;
-            if (t + i >= end) {
-                do {
-                    if (++n >= p.seq.sequences) return;  // rows behind the last sequence stay as they were
-                    start = packed_at(p.seq, n);
-                    end = packed_at(p.seq, n + 1);
-                } while (t + i >= end);
-                conv_history<T, V, K>(p, n, start, t + i, c, h);
+            if (t + i >= q.end) {
+                if (!q.to(p, t + i)) return;  // rows behind the last sequence stay as they were
+                ch.history(p, q, t + i, c);
             }
-            float y[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float x = R::get(raw[i], e);
-                float u = fmaf(w[K - 1][e], x, b[e]);
-#pragma unroll
-                for (int d = 0; d < K - 1; ++d) u = fmaf(w[K - 2 - d][e], h[d][e], u);
-#pragma unroll
-                for (int d = K - 2; d > 0; --d) h[d][e] = h[d - 1][e];
-                if constexpr (K > 1) h[0][e] = x;
-                y[e] = p.silu ? u * sigmoid_of<kAccurate>(u) : u;
-            }
-            R::store(p.y, (t + i) * p.y_stride + c, y);
+            row(t + i, now[i]);
         }
     }
 }
@@ -161,22 +239,25 @@ __global__ void __launch_bounds__(kConvThreads) conv1d_step_kernel(const Conv1dP
     if (c >= p.dim) return;
     const int64_t b = blockIdx.x / p.cblocks;
     const typename R::Raw x = R::load_raw(p.x, b * p.x_stride + c);
-    float w[K][V], u[V];
-    conv_taps<T, V, K>(p, c, w, u);
+    ConvChannels<T, V, K> ch;
+    ch.taps(p, c);
     const int slot = packed_slot(p.seq, static_cast<int>(b));
     if (slot < 0) return;
     const int64_t win = static_cast<int64_t>(slot) * (K - 1);
     typename R::Raw old[K > 1 ? K - 1 : 1];
-    if constexpr (K > 1) {
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) old[j] = R::load_raw_rw(p.windows, (win + j) * p.dim + c);
+    for (int j = 0; j < K - 1; ++j) old[j] = R::load_raw_rw(p.windows, (win + j) * p.dim + c);
+    Lanes<R::kL> v[R::kN], u[R::kN];
+#pragma unroll
+    for (int i = 0; i < R::kN; ++i) {
+        v[i] = R::pair(x, i);
+#pragma unroll
+        for (int d = 0; d < K - 1; ++d) ch.h[d][i] = R::pair(old[K - 2 - d], i);
     }
+    ch.row(v, u);
+    if (p.silu) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j) u[e] = fmaf(w[j][e], R::get(old[j], e), u[e]);
-        u[e] = fmaf(w[K - 1][e], R::get(x, e), u[e]);
-        if (p.silu) u[e] *= sigmoid_of<kAccurate>(u[e]);
+        for (int i = 0; i < R::kN; ++i) u[i] = u[i] * sigmoid_lanes<kAccurate, R::kL>(u[i]);
     }
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) R::store_raw(p.windows, (win + j) * p.dim + c, j + 1 < K - 1 ? old[j + 1] : x);
@@ -193,95 +274,137 @@ template <typename T, int V, int K>
 __global__ void __launch_bounds__(kConvThreads) conv1d_bwd_kernel(const Conv1dParams p) {
     using R = Row<T, V>;
     constexpr bool kAccurate = Act<T>::kBytes == 4;
+    constexpr int kL = R::kL, kN = R::kN, kB = kConvBwdBatch;
+    using Ln = Lanes<kL>;
+    __shared__ int64_t ends[32];
+    __shared__ int slots[32];
     const int64_t t0 = static_cast<int64_t>(blockIdx.x / p.cblocks) * p.tile;
     const int64_t t1 = min(t0 + p.tile, p.seq.tokens);
-    int n = packed_find(p.seq, t0);
+    ConvWalk q;
+    q.n = q.base = packed_find(p.seq, t0);
+    q.ends = ends, q.slots = slots;
+    q.start = 0, q.end = -1, q.slot = -1;
+    ConvWalk::stage(p, q.base, ends, slots);
     const int64_t c = (static_cast<int64_t>(blockIdx.x % p.cblocks) * kConvThreads + threadIdx.x) * V;
     if (c >= p.dim) return;
-    float w[K][V], b[V], h[K > 1 ? K - 1 : 1][V], g[K][V] = {}, dw[K][V] = {}, db[V] = {};
-    conv_taps<T, V, K>(p, c, w, b);
-    int64_t start = 0, end = -1, eh[K];
+    ConvChannels<T, V, K> ch;
+    Ln g[K][kN], dw[K][kN], db[kN];
+    int64_t eh[K];
 #pragma unroll
-    for (int d = 0; d < K; ++d) eh[d] = -1;
-    if (n < p.seq.sequences) {
-        start = packed_at(p.seq, n);
-        end = packed_at(p.seq, n + 1);
-        conv_history<T, V, K>(p, n, start, t0, c, h);
+    for (int d = 0; d < K; ++d) {
+        eh[d] = -1;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) g[d][i] = dw[d][i] = lanes<kL>(0.0f);
     }
-    const int64_t last = t1 + K - 1;  // the rows after the tile complete its last gradients
-    for (int64_t t = t0; t < last; t += 4) {
-        typename R::Raw rx[4], rd[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool in = t + i < last && t + i < p.seq.tokens;
-            rx[i] = in ? R::load_raw(p.x, (t + i) * p.x_stride + c) : R::zero_raw();
-            rd[i] = in ? R::load_raw(p.dy, (t + i) * p.dy_stride + c) : R::zero_raw();
+    for (int i = 0; i < kN; ++i) db[i] = lanes<kL>(0.0f);
+    const int64_t last = t1 + K - 1;  // the rows after the tile complete its last gradients
+    typename R::Raw rx[kB], rd[kB];
+    auto load = [&](int64_t t) {
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+            if (t + i >= last || t + i >= p.seq.tokens) continue;
+            rx[i] = R::load_raw(p.x, (t + i) * p.x_stride + c);
+            rd[i] = R::load_raw(p.dy, (t + i) * p.dy_stride + c);
+        }
+    };
+    load(t0);
+    ch.taps(p, c);
+    if (q.n < p.seq.sequences) {
+        q.enter(p);
+        ch.history(p, q, t0, c);
+    }
+    // g of a row that is in a sequence, and its part of the sums
+    auto row = [&](const typename R::Raw &rxi, const typename R::Raw &rdi, bool count) {
+        Ln x[kN], u[kN], hx[ConvChannels<T, V, K>::kH][kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            x[i] = R::pair(rxi, i);
+#pragma unroll
+            for (int d = 0; d < K - 1; ++d) hx[d][i] = ch.h[d][i];
+        }
+        ch.row(x, u);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            Ln gv = R::pair(rdi, i);
+            if (p.silu) {
+                const Ln sg = sigmoid_lanes<kAccurate, kL>(u[i]);
+                const Ln one = lanes<kL>(1.0f);
+                gv = gv * (sg * Ln::fma(u[i], Ln::fma(sg, lanes<kL>(-1.0f), one), one));
+            }
+#pragma unroll
+            for (int d = K - 1; d > 0; --d) g[d][i] = g[d - 1][i];
+            g[0][i] = gv;
+            if (count) {
+                db[i] = db[i] + gv;
+                dw[K - 1][i] = Ln::fma(gv, x[i], dw[K - 1][i]);
+#pragma unroll
+                for (int d = 0; d < K - 1; ++d) dw[K - 2 - d][i] = Ln::fma(gv, hx[d][i], dw[K - 2 - d][i]);
+            }
+        }
+    };
+    for (int64_t t = t0; t < last; t += kB) {
+        typename R::Raw nx[kB], nd[kB];
+#pragma unroll
+        for (int i = 0; i < kB; ++i) nx[i] = rx[i], nd[i] = rd[i];
+        load(t + kB);
+        // rows of one sequence whose K - 1 rows before are the same sequence's and the tile's
+        if (t - (K - 1) >= max(t0, q.start) && t + kB <= min(t1, q.end)) {
+#pragma unroll
+            for (int r = 0; r < kB; ++r) {
+                row(nx[r], nd[r], true);
+                Ln dx[kN];
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    dx[i] = ch.w[0][i] * g[0][i];
+#pragma unroll
+                    for (int d = 1; d < K; ++d) dx[i] = Ln::fma(ch.w[d][i], g[d][i], dx[i]);
+                }
+                R::store(p.dx, (t + r - (K - 1)) * p.dx_stride + c, dx);
+            }
+#pragma unroll
+            for (int d = 0; d < K; ++d) eh[d] = q.end;
+            continue;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t s = t + i;
+        for (int r = 0; r < kB; ++r) {
+            const int64_t s = t + r;
             if (s >= last) break;
-            if (n < p.seq.sequences && s >= end) {
-                do {
-                    if (++n >= p.seq.sequences) break;
-                    start = packed_at(p.seq, n);
-                    end = packed_at(p.seq, n + 1);
-                } while (s >= end);
-                if (n < p.seq.sequences) conv_history<T, V, K>(p, n, start, s, c, h);
-            }
-            const bool live = n < p.seq.sequences && s < p.seq.tokens;
+            if (q.n < p.seq.sequences && s >= q.end && q.to(p, s)) ch.history(p, q, s, c);
+            const bool live = q.n < p.seq.sequences && s < p.seq.tokens;
 #pragma unroll
-            for (int d = K - 1; d > 0; --d) {
-                eh[d] = eh[d - 1];
-#pragma unroll
-                for (int e = 0; e < V; ++e) g[d][e] = g[d - 1][e];
-            }
-            eh[0] = live ? end : -1;
+            for (int d = K - 1; d > 0; --d) eh[d] = eh[d - 1];
+            eh[0] = live ? q.end : -1;
             if (live) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float x = R::get(rx[i], e), dy = R::get(rd[i], e);
-                    float u = fmaf(w[K - 1][e], x, b[e]);
-#pragma unroll
-                    for (int d = 0; d < K - 1; ++d) u = fmaf(w[K - 2 - d][e], h[d][e], u);
-                    float gv = dy;
-                    if (p.silu) {
-                        const float sg = sigmoid_of<kAccurate>(u);
-                        gv = dy * (sg * fmaf(u, 1.0f - sg, 1.0f));
-                    }
-                    g[0][e] = gv;
-                    if (s < t1) {
-                        db[e] += gv;
-                        dw[K - 1][e] = fmaf(gv, x, dw[K - 1][e]);
-#pragma unroll
-                        for (int d = 0; d < K - 1; ++d) dw[K - 2 - d][e] = fmaf(gv, h[d][e], dw[K - 2 - d][e]);
-                    }
-#pragma unroll
-                    for (int d = K - 2; d > 0; --d) h[d][e] = h[d - 1][e];
-                    if constexpr (K > 1) h[0][e] = x;
-                }
+                row(nx[r], nd[r], s < t1);
             } else {
 #pragma unroll
-                for (int e = 0; e < V; ++e) g[0][e] = 0.0f;
-            }
-            const int64_t r = s - (K - 1);  // the row whose gradient is complete
-            if (r >= t0 && eh[K - 1] >= 0) {
-                float dx[V] = {};
+                for (int i = 0; i < kN; ++i) {
 #pragma unroll
-                for (int d = 0; d < K; ++d)  // g[d] is row s - d; its tap on row r is K - 1 - (K - 1 - d) = d
+                    for (int d = K - 1; d > 0; --d) g[d][i] = g[d - 1][i];
+                    g[0][i] = lanes<kL>(0.0f);
+                }
+            }
+            const int64_t done = s - (K - 1);  // the row whose gradient is complete
+            if (done >= t0 && eh[K - 1] >= 0) {
+                Ln dx[kN];
+#pragma unroll
+                for (int i = 0; i < kN; ++i) dx[i] = lanes<kL>(0.0f);
+#pragma unroll
+                for (int d = 0; d < K; ++d)  // g[d] is row s - d = done + (K - 1 - d): its tap on that row is d
                     if (s - d < eh[K - 1]) {
 #pragma unroll
-                        for (int e = 0; e < V; ++e) dx[e] = fmaf(w[d][e], g[d][e], dx[e]);
+                        for (int i = 0; i < kN; ++i) dx[i] = Ln::fma(ch.w[d][i], g[d][i], dx[i]);
                     }
-                R::store(p.dx, r * p.dx_stride + c, dx);
+                R::store(p.dx, done * p.dx_stride + c, dx);
             }
         }
     }
-    float *q = p.partial + static_cast<int64_t>(blockIdx.x / p.cblocks) * (K + 1) * p.dim + c;
+    float *o = p.partial + static_cast<int64_t>(blockIdx.x / p.cblocks) * (K + 1) * p.dim + c;
 #pragma unroll
     for (int k = 0; k <= K; ++k)
 #pragma unroll
-        for (int e = 0; e < V; ++e) q[k * p.dim + e] = k < K ? dw[k][e] : db[e];
+        for (int e = 0; e < V; ++e) o[k * p.dim + e] = (k < K ? dw[k][e / kL] : db[e / kL]).get(e % kL);
 }
 
 // dst[c * stride_c + k] = sum over tiles of partial[tile][k][c], tiles in order

@@ -89,10 +89,11 @@ __global__ void __launch_bounds__(512) gated_norm_fwd_kernel(const NormParams p,
     for (int i = 0; i < NV; ++i) {
         const int64_t c = (static_cast<int64_t>(i) * tpr + j) * V;
         if (c >= p.gdim) continue;
-        float o[V];
+        float o[V], w[V];
+        load_params<V, (V > 1)>(p.weight + col0 + c, w);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            o[e] = v[i][e] * r * __ldg(p.weight + col0 + c + e);
+            o[e] = v[i][e] * r * w[e];
             if constexpr (GATE && !GATE_FIRST) {
                 const float z = R::get(rz[i], e);
                 o[e] *= z * sigmoid_of<kAccurate>(z);
@@ -103,81 +104,152 @@ __global__ void __launch_bounds__(512) gated_norm_fwd_kernel(const NormParams p,
 }
 
 // Gradients.  Block (b, g) takes rows b R, b R + 1, ... of group g (R rows share
-// the block when a row needs one warp or less) at a stride of the grid, and keeps
-// the sums of dw over its rows in registers; they go to `partial`, one row of it
-// per block and row slot, added in a fixed order by norm_reduce_kernel.
-template <typename T, int V, int NV, bool GATE, bool GATE_FIRST>
-__global__ void __launch_bounds__(512) gated_norm_bwd_kernel(const NormParams p, int tpr) {
+// the block when a row needs one warp or less) at a stride of the grid.  Whole
+// 16-byte vectors come through shared memory, each thread's own by cp.async, so
+// that the next rows are on their way without holding registers; both sums cross
+// the block at once.  dw over the block's rows stays in registers and goes to
+// `partial`, one row of it per block and row slot, added in a fixed order by
+// norm_reduce_kernel.  THREADS, BLOCKS: the block's threads at most and the blocks
+// that share an SM, which bound the registers.
+// Rows in shared memory: this one and the next; only this one where a thread has
+// eight vectors (float32 rows beyond 8192 columns), which would not fit twice.
+__host__ __device__ constexpr int norm_stages(int nv) { return nv < 8 ? 2 : 1; }
+// shared memory of a block: x, dout and z vectors of its threads, a stage after another
+__host__ __device__ constexpr int norm_bwd_smem(int threads, int nv, int bytes, bool gate) {
+    return bytes == 16 ? norm_stages(nv) * (gate ? 3 : 2) * nv * threads * 16 : 0;
+}
+
+template <typename T, int V, int NV, bool GATE, bool GATE_FIRST, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) gated_norm_bwd_kernel(const NormParams p, int tpr) {
     using R = Row<T, V>;
-    constexpr bool kAccurate = Act<T>::kBytes == 4;
-    __shared__ float slots[2][2][32];
+    constexpr bool kAccurate = Act<T>::kBytes == 4, kAsync = V * Act<T>::kBytes == 16;
+    constexpr int kArrays = GATE ? 3 : 2, kStages = norm_stages(NV);
+    extern __shared__ __align__(16) uint4 rows_smem[];
+    __shared__ float2 slots[2][32];
     const int j = threadIdx.x % tpr, rpb = blockDim.x / tpr;
     const int64_t col0 = static_cast<int64_t>(blockIdx.y) * p.gdim;
     const int64_t slot = static_cast<int64_t>(blockIdx.x) * rpb + threadIdx.x / tpr;
     const int64_t step = static_cast<int64_t>(gridDim.x) * rpb;
-    float dw[NV][V] = {};
-    int flip = 0;  // the sums' shared slots alternate: one barrier per sum is enough
-    const int64_t trips = (p.rows + step - 1) / step;
-    for (int64_t k = 0; k < trips; ++k, flip ^= 1) {
-        const bool live = slot + k * step < p.rows;
-        const int64_t row = live ? slot + k * step : p.rows - 1;
-        typename R::Raw rx[NV], rz[NV], rd[NV];
+    const float inv = 1.0f / static_cast<float>(p.gdim);
+    using Ln = Lanes<R::kL>;
+    constexpr int kL = R::kL, kN = R::kN;
+    Ln dw[NV][kN];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < kN; ++e) dw[i][e] = lanes<kL>(0.0f);
+    typename R::Raw reg[kAsync ? 1 : kArrays][kAsync ? 1 : NV];
+    // this thread's vector i of array a (x, dout, z) of trip k
+    auto at = [&](int64_t k, int a, int i) -> uint4 & {
+        return rows_smem[((static_cast<int>(k % kStages) * kArrays + a) * NV + i) * blockDim.x + threadIdx.x];
+    };
+    auto load = [&](int64_t k) {
+        const int64_t row = slot + k * step;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = (static_cast<int64_t>(i) * tpr + j) * V;
-            const bool in = c < p.gdim;
-            rx[i] = in ? R::load_raw(p.x, row * p.x_stride + col0 + c) : R::zero_raw();
-            if constexpr (GATE) rz[i] = in ? R::load_raw(p.z, row * p.z_stride + col0 + c) : R::zero_raw();
-            rd[i] = in ? R::load_raw(p.dout, row * p.dout_stride + col0 + c) : R::zero_raw();
-        }
-        float ss = 0.0f, dot = 0.0f;  // sum of v^2, and of (up w) v
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c = (static_cast<int64_t>(i) * tpr + j) * V;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                float v = R::get(rx[i], e), up = R::get(rd[i], e);
-                if constexpr (GATE) {
-                    const float z = R::get(rz[i], e), s = z * sigmoid_of<kAccurate>(z);
-                    if constexpr (GATE_FIRST) v *= s;
-                    else up *= s;
-                }
-                ss = fmaf(v, v, ss);
-                dot = fmaf(up * (c < p.gdim ? __ldg(p.weight + col0 + c + e) : 0.0f), v, dot);
+            const bool in = c < p.gdim && row < p.rows;
+            const int64_t ix = in ? row * p.x_stride + col0 + c : 0, id = in ? row * p.dout_stride + col0 + c : 0,
+                          iz = in ? row * p.z_stride + col0 + c : 0;
+            if constexpr (kAsync) {
+                const uint32_t n = in ? 16u : 0u;
+                copy16_async(&at(k, 0, i), static_cast<const char *>(p.x) + ix * Act<T>::kBytes, n);
+                copy16_async(&at(k, 1, i), static_cast<const char *>(p.dout) + id * Act<T>::kBytes, n);
+                if constexpr (GATE) copy16_async(&at(k, 2, i), static_cast<const char *>(p.z) + iz * Act<T>::kBytes, n);
+            } else {
+                reg[0][i] = in ? R::load_raw(p.x, ix) : R::zero_raw();
+                reg[1][i] = in ? R::load_raw(p.dout, id) : R::zero_raw();
+                if constexpr (GATE) reg[2][i] = in ? R::load_raw(p.z, iz) : R::zero_raw();
             }
         }
-        ss = norm_row_sum(ss, tpr, slots[flip][0]);
-        dot = norm_row_sum(dot, tpr, slots[flip][1]);
-        const float r = 1.0f / sqrtf(ss / static_cast<float>(p.gdim) + p.eps);
-        const float mean = dot * r / static_cast<float>(p.gdim);  // m(dn n)
-        if (!live) continue;
+        if constexpr (kAsync) copy_async_commit();
+    };
+    auto get = [&](int64_t k, int a, int i) -> typename R::Raw {
+        if constexpr (kAsync) {
+            const uint4 v = at(k, a, i);
+            typename R::Raw r;
+            r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+            return r;
+        } else {
+            return reg[a][i];
+        }
+    };
+    const int64_t trips = (p.rows + step - 1) / step;  // the same for every thread: all join the sums
+    if constexpr (kAsync && kStages > 1) load(0);
+    for (int64_t k = 0; k < trips; ++k) {
+        const int64_t row = slot + k * step;
+        load(k + (kAsync ? kStages - 1 : 0));  // (past the last row: zeros, so that the count of groups stays)
+        if constexpr (kAsync) copy_async_wait<kStages - 1>();
+        Ln sg[GATE ? NV : 1][kN];     // sigmoid(z)
+        Ln ss2 = lanes<kL>(0.0f), dot2 = lanes<kL>(0.0f);  // sums of v^2, and of (up w) v
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t c = (static_cast<int64_t>(i) * tpr + j) * V;
+            float w[V] = {};
+            if (c < p.gdim) load_params<V, (V > 1)>(p.weight + col0 + c, w);
+            const typename R::Raw cx = get(k, 0, i), cd = get(k, 1, i), cz = get(k, GATE ? 2 : 0, i);
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                Ln v = R::pair(cx, e), up = R::pair(cd, e);
+                if constexpr (GATE) {
+                    const Ln z = R::pair(cz, e);
+                    sg[i][e] = sigmoid_lanes<kAccurate, kL>(z);
+                    if constexpr (GATE_FIRST) v = v * (z * sg[i][e]);
+                    else up = up * (z * sg[i][e]);
+                }
+                ss2 = Ln::fma(v, v, ss2);
+                dot2 = Ln::fma(up * Ln::of(w[e * kL], w[e * kL + kL - 1]), v, dot2);
+            }
+        }
+        float ss = ss2.get(0), dot = dot2.get(0);
+        if constexpr (kL > 1) ss += ss2.get(1), dot += dot2.get(1);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            if (o < tpr) {
+                ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            }
+        if (tpr > 32) {  // one row to the block; the slots alternate, so one barrier per row is enough
+            float2 *sl = slots[k & 1];
+            if ((threadIdx.x & 31) == 0) sl[threadIdx.x >> 5] = make_float2(ss, dot);
+            __syncthreads();
+            ss = dot = 0.0f;
+            for (int i = 0; i < tpr >> 5; ++i) ss += sl[i].x, dot += sl[i].y;
+        }
+        const float r = 1.0f / sqrtf(ss * inv + p.eps);
+        const float mean = dot * r * inv;  // m(dn n)
+        if (row >= p.rows) continue;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = (static_cast<int64_t>(i) * tpr + j) * V;
             if (c >= p.gdim) continue;
-            float dx[V], dz[V];
+            float w[V];
+            Ln dx[kN], dz[kN];
+            load_params<V, (V > 1)>(p.weight + col0 + c, w);
+            const typename R::Raw cx = get(k, 0, i), cd = get(k, 1, i), cz = get(k, GATE ? 2 : 0, i);
+            const Ln r2 = lanes<kL>(r), m2 = lanes<kL>(-mean), one = lanes<kL>(1.0f);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float x = R::get(rx[i], e), d = R::get(rd[i], e), w = __ldg(p.weight + col0 + c + e);
+            for (int e = 0; e < kN; ++e) {
+                const Ln x = R::pair(cx, e), d = R::pair(cd, e), we = Ln::of(w[e * kL], w[e * kL + kL - 1]);
                 if constexpr (GATE) {
-                    const float z = R::get(rz[i], e), sg = sigmoid_of<kAccurate>(z), s = z * sg;
-                    const float ds = sg * fmaf(z, 1.0f - sg, 1.0f);
+                    const Ln z = R::pair(cz, e), g = sg[i][e], s = z * g;
+                    const Ln ds = g * Ln::fma(z, Ln::fma(g, lanes<kL>(-1.0f), one), one);
                     if constexpr (GATE_FIRST) {
-                        const float n = x * s * r;
-                        const float dv = r * fmaf(-n, mean, d * w);
-                        dw[i][e] = fmaf(d, n, dw[i][e]);
+                        const Ln n = x * s * r2;
+                        const Ln dv = r2 * Ln::fma(n, m2, d * we);
+                        dw[i][e] = Ln::fma(d, n, dw[i][e]);
                         dx[e] = dv * s;
                         dz[e] = dv * x * ds;
                     } else {
-                        const float n = x * r, up = d * s;
-                        dw[i][e] = fmaf(up, n, dw[i][e]);
-                        dx[e] = r * fmaf(-n, mean, up * w);
-                        dz[e] = d * n * w * ds;
+                        const Ln n = x * r2, up = d * s;
+                        dw[i][e] = Ln::fma(up, n, dw[i][e]);
+                        dx[e] = r2 * Ln::fma(n, m2, up * we);
+                        dz[e] = d * n * we * ds;
                     }
                 } else {
-                    const float n = x * r;
-                    dw[i][e] = fmaf(d, n, dw[i][e]);
-                    dx[e] = r * fmaf(-n, mean, d * w);
+                    const Ln n = x * r2;
+                    dw[i][e] = Ln::fma(d, n, dw[i][e]);
+                    dx[e] = r2 * Ln::fma(n, m2, d * we);
                 }
             }
             R::store(p.dx, row * p.dx_stride + col0 + c, dx);
@@ -189,7 +261,7 @@ __global__ void __launch_bounds__(512) gated_norm_bwd_kernel(const NormParams p,
         const int64_t c = (static_cast<int64_t>(i) * tpr + j) * V;
         if (c >= p.gdim) continue;
 #pragma unroll
-        for (int e = 0; e < V; ++e) p.partial[slot * p.dim + col0 + c + e] = dw[i][e];
+        for (int e = 0; e < V; ++e) p.partial[slot * p.dim + col0 + c + e] = dw[i][e / kL].get(e % kL);
     }
 }
 

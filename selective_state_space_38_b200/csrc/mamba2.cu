@@ -114,12 +114,22 @@ int conv_dispatch(int32_t act_dtype, bool vec, int k, F f) {
 
 int launched() { return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA; }
 
-// rows of a tile of the gradient kernel, and tiles: at least 128 rows, at most
-// 256 tiles, so that the partial sums stay small beside the rows
-int64_t conv_bwd_tile(int64_t tokens) { return std::max<int64_t>(128, ((tokens + 255) / 256 + 3) / 4 * 4); }
-int64_t conv_bwd_tiles(int64_t tokens) { return (tokens + conv_bwd_tile(tokens) - 1) / conv_bwd_tile(tokens); }
+// Rows of a tile.  A tile reads K - 1 rows before its own (and, for the gradients,
+// after them) and its taps again, so tiles are long; but few rows are cut shorter,
+// down to 16, until some four blocks of 128 threads stand for each SM.
+int64_t conv_tile(int64_t tokens, int64_t dim, int64_t longest) {
+    const int64_t cblocks = (dim + 4 * kConvThreads - 1) / (4 * kConvThreads);
+    int64_t tile = longest;
+    while (tile > 16 && (tokens + tile - 1) / tile * cblocks < 592) tile /= 2;
+    return tile;
+}
+// For the gradients at most 256 tiles: their partial sums stay small beside the rows.
+int64_t conv_bwd_tile(int64_t tokens, int64_t dim) {
+    return std::max<int64_t>(conv_tile(tokens, dim, 128), ((tokens + 255) / 256 + 3) / 4 * 4);
+}
+int64_t conv_bwd_tiles(int64_t tokens, int64_t dim) { return (tokens + conv_bwd_tile(tokens, dim) - 1) / conv_bwd_tile(tokens, dim); }
 size_t conv_bwd_bytes(const ssm_conv1d_dims_t *d) {
-    return static_cast<size_t>(conv_bwd_tiles(d->tokens)) * (d->width + 1) * d->dim * 4;
+    return static_cast<size_t>(conv_bwd_tiles(d->tokens, d->dim)) * (d->width + 1) * d->dim * 4;
 }
 
 }  // namespace
@@ -145,14 +155,18 @@ int ssm_conv1d_fwd(const void *x, const float *w, const float *bias, const int32
     if (outputs_clash(ins, outs)) return SSM_ERR_INVALID_ARG;
     p.windows = windows, p.y = y, p.y_stride = dims->y_stride;
     p.seq.cu = cu_seqlens, p.seq.slots = slots, p.seq.has_initial = has_initial;
-    const bool vec = vector_rows({x, y, windows}, {dims->x_stride, dims->y_stride}, dims->dim, dims->act_dtype);
-    const int64_t tiles = (dims->tokens + kConvTile - 1) / kConvTile;
+    const bool vec = vector_rows({x, y, windows, w, bias}, {dims->x_stride, dims->y_stride}, dims->dim, dims->act_dtype);
+    p.tile = conv_tile(dims->tokens, dims->dim, 64);
+    const int64_t tiles = (dims->tokens + p.tile - 1) / p.tile;
     if ((std::max<int64_t>(tiles, dims->sequences)) * conv_cblocks(dims->dim, 1) > INT32_MAX) return SSM_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return conv_dispatch(dims->act_dtype, vec, dims->width, [&](auto t, auto v, auto k) {
         using T = decltype(t);
+        // four channels a thread (8 bytes of bf16): with eight, 144 registers leave 14 warps an SM
+        constexpr int V = v > 4 ? 4 : v;
+        p.cblocks = conv_cblocks(p.dim, V);
+        conv1d_fwd_kernel<T, V, k><<<static_cast<unsigned>(tiles * p.cblocks), kConvThreads, 0, s>>>(p);
         p.cblocks = conv_cblocks(p.dim, v);
-        conv1d_fwd_kernel<T, v, k><<<static_cast<unsigned>(tiles * p.cblocks), kConvThreads, 0, s>>>(p);
         if (windows && k > 1)
             conv1d_window_kernel<T, v, k><<<static_cast<unsigned>(p.seq.sequences * static_cast<int64_t>(p.cblocks)), kConvThreads, 0, s>>>(p);
         return launched();
@@ -177,7 +191,7 @@ int ssm_conv1d_step(void *windows, const int32_t *slots, const void *x, const fl
     if (outputs_clash(ins, outs)) return SSM_ERR_INVALID_ARG;
     p.windows = windows, p.y = y, p.y_stride = dims->y_stride;
     p.seq.slots = slots, p.seq.sequences = static_cast<int32_t>(dims->tokens);
-    const bool vec = vector_rows({x, y, windows}, {dims->x_stride, dims->y_stride}, dims->dim, dims->act_dtype);
+    const bool vec = vector_rows({x, y, windows, w, bias}, {dims->x_stride, dims->y_stride}, dims->dim, dims->act_dtype);
     if (dims->tokens * conv_cblocks(dims->dim, 1) > INT32_MAX) return SSM_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return conv_dispatch(dims->act_dtype, vec, dims->width, [&](auto t, auto v, auto k) {
@@ -218,13 +232,13 @@ int ssm_conv1d_bwd(const void *x, const float *w, const float *bias, const int32
     p.dy = dy, p.dx = dx, p.dy_stride = dims->dy_stride, p.dx_stride = dims->dx_stride;
     p.partial = static_cast<float *>(workspace), p.dw = dw, p.dbias = dbias;
     p.seq.cu = cu_seqlens;
-    p.tile = conv_bwd_tile(dims->tokens);
-    const int64_t tiles = conv_bwd_tiles(dims->tokens);
-    const bool vec = vector_rows({x, dy, dx}, {dims->x_stride, dims->dy_stride, dims->dx_stride}, dims->dim, dims->act_dtype);
+    p.tile = conv_bwd_tile(dims->tokens, dims->dim);
+    const int64_t tiles = conv_bwd_tiles(dims->tokens, dims->dim);
+    const bool vec = vector_rows({x, dy, dx, w, bias}, {dims->x_stride, dims->dy_stride, dims->dx_stride}, dims->dim, dims->act_dtype);
     if (tiles * conv_cblocks(dims->dim, 1) > INT32_MAX) return SSM_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return conv_dispatch(dims->act_dtype, vec, dims->width, [&](auto t, auto v, auto k) {
-        constexpr int V = v > 4 ? 4 : v;  // four channels a thread: the taps' sums and the histories stay in registers
+        constexpr int V = v > 2 ? 2 : v;  // two channels a thread: with four, 157 registers leave 12 warps an SM
         p.cblocks = conv_cblocks(p.dim, V);
         conv1d_bwd_kernel<decltype(t), V, k><<<static_cast<unsigned>(tiles * p.cblocks), kConvThreads, 0, s>>>(p);
         conv1d_reduce_kernel<<<dim3(static_cast<unsigned>((p.dim + 31) / 32), k + 1), dim3(32, 8), 0, s>>>(
@@ -241,7 +255,7 @@ namespace {
 
 constexpr int kNormThreads = 512;      // threads that share a row's group at most
 constexpr int kNormSmallBlock = 128;   // threads of a block whose rows need one warp or less
-constexpr int kNormBwdBlocks = 592;    // blocks of the gradient kernel in all: four for each of 148 SMs
+constexpr int kNormBwdBlocks = 296;    // blocks of the gradient kernel in all: two for each of 148 SMs
 
 // How the threads share a row's group of `gdim` columns: vectors of V elements,
 // NV to a thread, `tpr` threads.
@@ -337,7 +351,7 @@ int ssm_gated_norm_fwd(const void *x, const void *z, const float *weight, void *
     const Rows outs[] = {{out, dims->rows, wb, dims->out_stride * es}, flat(rstd, rstd ? dims->rows * dims->groups * 4 : 0)};
     if (outputs_clash(ins, outs)) return SSM_ERR_INVALID_ARG;
     p.out = out, p.rstd = rstd, p.out_stride = dims->out_stride;
-    const bool vec = vector_rows({x, z, out}, {dims->x_stride, z ? dims->z_stride : 0, dims->out_stride}, p.gdim, dims->act_dtype);
+    const bool vec = vector_rows({x, z, out, weight}, {dims->x_stride, z ? dims->z_stride : 0, dims->out_stride}, p.gdim, dims->act_dtype);
     NormShape s;
     if (!norm_shape(p.gdim, vec ? (es == 4 ? 4 : 8) : 1, 32, &s)) return SSM_ERR_UNSUPPORTED;
     const int64_t blocks = (p.rows * p.groups + s.rpb - 1) / s.rpb;
@@ -378,7 +392,7 @@ int ssm_gated_norm_bwd(const void *x, const void *z, const float *weight, const 
     if (outputs_clash(ins, outs)) return SSM_ERR_INVALID_ARG;
     p.dout = dout, p.dx = dx, p.dz = dz, p.partial = static_cast<float *>(workspace);
     p.dout_stride = dims->dout_stride, p.dx_stride = dims->dx_stride, p.dz_stride = dims->dz_stride;
-    const bool vec = vector_rows({x, z, dout, dx, dz},
+    const bool vec = vector_rows({x, z, dout, dx, dz, weight},
                                  {dims->x_stride, z ? dims->z_stride : 0, dims->dout_stride, dims->dx_stride, dz ? dims->dz_stride : 0},
                                  p.gdim, dims->act_dtype);
     NormShape s;
@@ -386,8 +400,19 @@ int ssm_gated_norm_bwd(const void *x, const void *z, const float *weight, const 
     const int64_t blocks = norm_bwd_blocks(p.rows, p.groups, s.rpb);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return norm_dispatch(dims->act_dtype, s, z != nullptr, dims->gate_first != 0, [&](auto t, auto v, auto nv, auto gate, auto first) {
-        gated_norm_bwd_kernel<decltype(t), v, nv, gate, first>
-            <<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.groups)), s.tpr * s.rpb, 0, st>>>(p, s.tpr);
+        // 16 elements a thread fit the 96 registers with which two blocks of 320 threads share an SM
+        // (three at 64 registers spilled: 210 us against 191 for 16384 rows of 5120)
+        const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(p.groups));
+        const int threads = s.tpr * s.rpb, smem = norm_bwd_smem(threads, nv, v * static_cast<int>(es), gate);
+        auto launch = [&](auto kernel) {
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return SSM_ERR_CUDA;
+            kernel<<<grid, threads, smem, st>>>(p, s.tpr);
+            return SSM_OK;
+        };
+        const int rc2 = nv * v <= 16 && threads <= 320
+                            ? launch(gated_norm_bwd_kernel<decltype(t), v, nv, gate, first, 320, 2>)
+                            : launch(gated_norm_bwd_kernel<decltype(t), v, nv, gate, first, kNormThreads, 1>);
+        if (rc2 != SSM_OK) return rc2;
         norm_reduce_kernel<<<static_cast<unsigned>((p.dim + 31) / 32), dim3(32, 32), 0, st>>>(p.partial, dweight, p.dim, blocks * s.rpb);
         return launched();
     });

@@ -6,7 +6,52 @@
 
 namespace ssm {
 
-// V consecutive elements at p (aligned to V elements; V = 1, 4 or, for bf16, 8)
+// One or two float32 values that go through an operation together (two: the f32x2
+// instructions, one issue slot for both, each rounded as by itself).
+template <int L>
+struct Lanes;
+template <>
+struct Lanes<1> {
+    float v;
+    __device__ __forceinline__ static Lanes of(float a, float) { return {a}; }
+    __device__ __forceinline__ float get(int) const { return v; }
+    __device__ __forceinline__ friend Lanes operator*(Lanes a, Lanes b) { return {a.v * b.v}; }
+    __device__ __forceinline__ friend Lanes operator+(Lanes a, Lanes b) { return {a.v + b.v}; }
+    __device__ __forceinline__ static Lanes fma(Lanes a, Lanes b, Lanes c) { return {fmaf(a.v, b.v, c.v)}; }
+};
+template <>
+struct Lanes<2> {
+    uint64_t v;
+    __device__ __forceinline__ static Lanes of(float a, float b) {
+        Lanes r;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+        return r;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        float a, b;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+        return i ? b : a;
+    }
+    __device__ __forceinline__ friend Lanes operator*(Lanes a, Lanes b) {
+        Lanes r;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+        return r;
+    }
+    __device__ __forceinline__ friend Lanes operator+(Lanes a, Lanes b) {
+        Lanes r;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+        return r;
+    }
+    __device__ __forceinline__ static Lanes fma(Lanes a, Lanes b, Lanes c) {
+        Lanes r;
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+        return r;
+    }
+};
+template <int L>
+__device__ __forceinline__ Lanes<L> lanes(float a) { return Lanes<L>::of(a, a); }
+
+// V consecutive elements at p (aligned to V elements; V = 1, 2, 4 or, for bf16, 8)
 // as floats, and back.
 template <typename T, int V>
 struct Row {
@@ -27,7 +72,7 @@ struct Row {
             const uint2 *q = reinterpret_cast<const uint2 *>(p);
             const uint2 v = CONST ? __ldg(q) : *q;
             r.w[0] = v.x, r.w[1] = v.y;
-        } else if constexpr (Act<T>::kBytes == 4) {
+        } else if constexpr (V * Act<T>::kBytes == 4) {
             const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
             r.w[0] = CONST ? __ldg(q) : *q;
         } else {
@@ -48,6 +93,16 @@ struct Row {
         else if constexpr (V == 1) return __uint_as_float(r.w[0] << 16);
         else return (e & 1) ? __uint_as_float(r.w[e / 2] & 0xffff0000u) : __uint_as_float(r.w[e / 2] << 16);
     }
+    static constexpr int kL = V % 2 == 0 ? 2 : 1, kN = V / kL;  // values that go together, and how many such
+    __device__ __forceinline__ static Lanes<kL> pair(const Raw &r, int i) {
+        return Lanes<kL>::of(get(r, i * kL), kL > 1 ? get(r, i * kL + kL - 1) : 0.0f);
+    }
+    __device__ __forceinline__ static void store(void *base, int64_t i, const Lanes<kL> (&v)[kN]) {
+        float f[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] = v[e / kL].get(e % kL);
+        store(base, i, f);
+    }
     // one rounding (to nearest even) when T is bf16
     __device__ __forceinline__ static void store(void *base, int64_t i, const float (&v)[V]) {
         char *p = static_cast<char *>(base) + i * Act<T>::kBytes;
@@ -58,6 +113,10 @@ struct Row {
                                                        pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
         } else if constexpr (Act<T>::kBytes == 2 && V == 4) {
             *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        } else if constexpr (Act<T>::kBytes == 4 && V == 2) {
+            *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+        } else if constexpr (Act<T>::kBytes == 2 && V == 2) {
+            *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(v[0], v[1]);
         } else {
 #pragma unroll
             for (int e = 0; e < V; ++e) Act<T>::store(base, i + e, v[e]);
@@ -69,13 +128,39 @@ struct Row {
             *reinterpret_cast<uint4 *>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
         } else if constexpr (V * Act<T>::kBytes == 8) {
             *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
-        } else if constexpr (Act<T>::kBytes == 4) {
+        } else if constexpr (V * Act<T>::kBytes == 4) {
             *reinterpret_cast<uint32_t *>(p) = r.w[0];
         } else {
             *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(r.w[0]);
         }
     }
 };
+
+// 16 bytes global -> shared without a register round trip (bytes = 0: zeros, nothing read).
+__device__ __forceinline__ void copy16_async(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {  // until at most N groups are pending
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// N consecutive float32 parameters: as 16-byte vectors when VEC (the host checks their
+// alignment with the rows'), else one by one.
+template <int N, bool VEC>
+__device__ __forceinline__ void load_params(const float *p, float (&v)[N]) {
+    if constexpr (VEC && N % 4 == 0) {  // (N / 4 vectors lie together, so N floats' alignment is 16 bytes)
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(p) + i);
+            v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __ldg(p + i);
+    }
+}
 
 // silu(v) and its derivative sg (1 + v (1 - sg)), sg = 1 / (1 + e^-v).  For
 // float32 activations with expf and a true division; for bf16 with the MUFU
@@ -84,6 +169,18 @@ template <bool ACCURATE>
 __device__ __forceinline__ float sigmoid_of(float v) {
     if constexpr (ACCURATE) return 1.0f / (1.0f + expf(-v));
     else return rcp_approx(1.0f + ex2_approx(-v * kLog2e));
+}
+
+// sigmoid of one or two values: the multiplications and the sum together.
+template <bool ACCURATE, int L>
+__device__ __forceinline__ Lanes<L> sigmoid_lanes(Lanes<L> v) {
+    if constexpr (ACCURATE) {
+        return Lanes<L>::of(sigmoid_of<true>(v.get(0)), L > 1 ? sigmoid_of<true>(v.get(L - 1)) : 0.0f);
+    } else {
+        const Lanes<L> t = v * lanes<L>(-kLog2e);
+        const Lanes<L> e = lanes<L>(1.0f) + Lanes<L>::of(ex2_approx(t.get(0)), L > 1 ? ex2_approx(t.get(L - 1)) : 0.0f);
+        return Lanes<L>::of(rcp_approx(e.get(0)), L > 1 ? rcp_approx(e.get(L - 1)) : 0.0f);
+    }
 }
 
 // Packed sequences: cu[0..n], where sequence i is rows [cu[i], cu[i + 1]).  The

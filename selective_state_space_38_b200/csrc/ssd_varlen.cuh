@@ -122,7 +122,7 @@ struct VarSmem {
     static constexpr int kTabD = kS + kVarHeads * kTile;            // d [head][128]
     static constexpr int kTabW = kTabD + kVarHeads * 512;           // w where the decays factor, else dt
     static constexpr int kInfo = kTabW + kVarHeads * 512;
-    static constexpr int kBar = kInfo + 128;
+    static constexpr int kBar = kInfo + 256;                        // of even and of odd chunks
     static constexpr int kTotal = kBar + 128;
 };
 static_assert(sizeof(VarChunk) <= 128, "");
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tbase = *reinterpret_cast<volatile uint32_t *>(tslot);
     // TMEM columns: C B^T (128; its two heads' matrices replace it, as bf16 pairs: of
-    // every 32 columns the first 16 for head 0, the others for head 1), Yd, Yo and S (128
+    // every 16 columns the first 8 for head 0, the others for head 1), Yd, Yo and S (128
     // each: head h's column p in 64 h + p; lane n holds S[p][n])
     const uint32_t tG = tbase, tYd = tbase + 128, tYo = tbase + 256, tS = tbase + 384;
     constexpr int kN = 64 * kVarHeads;
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             int t0 = 0, h0 = 0, nh = 0, g = 0;
             auto next = [&](uint32_t u) -> bool {  // the chunk's numbers; false: no more
                 if (!ssd_wait(bFull, u & 1u, error)) return false;
-                const VarChunk &c = *info;
+                const VarChunk &c = info[u & 1u];
                 const bool go = !c.stop;
                 t0 = c.t0, h0 = c.h0, nh = c.nh, g = c.g;
                 ssd_arrive(bEmpty);
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                             const uint64_t dX = ssd_desc(aX + i * S::kTile, S::kTile, 1024);
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                ssd_mma_ts(tYd + 64 * i, tG + 32 * (k / 2) + 16 * i + 8 * (k % 2), dX + ((2048 * k) >> 4), id, k > 0);
+                                ssd_mma_ts(tYd + 64 * i, tG + 16 * k + 8 * i, dX + ((2048 * k) >> 4), id, k > 0);
                         }
                     }
                 }
@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kVarThreads, 1)
         VarItem it = fetch();
         if (it.valid) load_dt(it, it.first);
         while (ok && it.valid) {
-            const VarItem nxt = fetch();
+            VarItem nxt;
+            nxt.valid = false;
             float item_total = 0.0f;
             for (int64_t t = it.first; t < it.stop; t += kVarQ) {
                 const int rows = static_cast<int>(min(static_cast<int64_t>(kVarQ), it.stop - t));
@@ -429,7 +430,6 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                     if (8 * sub + k >= rows || hh >= it.nh) dt[k] = 0.0f;
                 }
                 if (!last_chunk) load_dt(it, t + rows);
-                else if (nxt.valid) load_dt(nxt, nxt.first);
                 // d_j = minus the sum of the later rows' dt A
                 float after = 0.0f;
 #pragma unroll
@@ -484,32 +484,36 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 for (int k = 0; k < 8; ++k)
                     if (!factored) w[k] = dt[k];
                 pw[0] = make_float4(w[0], w[1], w[2], w[3]), pw[1] = make_float4(w[4], w[5], w[6], w[7]);
+                VarChunk *out = info + (u & 1u);
                 if (sub == 0) {
-                    info->decay[hh] = expf(T), info->total[hh] = T, info->D[hh] = it.D;
-                    info->factored[hh] = factored;
+                    out->decay[hh] = expf(T), out->total[hh] = T, out->D[hh] = it.D;
+                    out->factored[hh] = factored;
                     if (SUMMARY && last_chunk && hh < it.nh) p.work.decay[(it.window + 1) * p.heads + it.h0 + hh] = expf(item_total);
                 }
                 if (lane == 0) {
-                    info->t0 = static_cast<int>(t), info->rows = rows;
-                    info->h0 = it.h0, info->nh = it.nh, info->g = it.g;
-                    info->first = t == it.first, info->last = last_chunk;
-                    info->stop = 0;
-                    info->src = it.src;
+                    out->t0 = static_cast<int>(t), out->rows = rows;
+                    out->h0 = it.h0, out->nh = it.nh, out->g = it.g;
+                    out->first = t == it.first, out->last = last_chunk;
+                    out->stop = 0;
+                    out->src = it.src;
                     const bool hand = SUMMARY || (it.more && !parallel);
-                    info->dst = hand ? p.work.carry + ((it.window + 1) * p.heads + it.h0) * (kSsdP * kSsdN)
+                    out->dst = hand ? p.work.carry + ((it.window + 1) * p.heads + it.h0) * (kSsdP * kSsdN)
                                      : it.more ? nullptr : it.state;
-                    info->flag = hand && !SUMMARY ? p.work.flags + (it.window + 1) * p.pairs + it.g * pairs_per_group +
+                    out->flag = hand && !SUMMARY ? p.work.flags + (it.window + 1) * p.pairs + it.g * pairs_per_group +
                                                         (it.h0 - it.g * HG) / kVarHeads
                                                   : nullptr;
                 }
                 __syncwarp();
                 if (lane == 0) ssd_arrive(bFull);
                 ++u;
+                // the next item, and its first dt, while this chunk is worked on
+                if (t == it.first) nxt = fetch();
+                if (last_chunk && nxt.valid) load_dt(nxt, nxt.first);
             }
             it = nxt;
         }
         if (ready() && lane == 0) {
-            info->stop = 1;
+            info[u & 1u].stop = 1;
             ssd_arrive(bFull);
         }
         __syncwarp();
@@ -525,18 +529,16 @@ __global__ void __launch_bounds__(kVarThreads, 1)
         for (uint32_t u = 0;; ++u) {
             const uint32_t ph = u & 1u;
             ok = __all_sync(0xffffffffu, ssd_wait(bFull, ph, error));
-            if (!ok || info->stop) break;
-            const VarChunk &c = *info;
-            const int t0 = c.t0, rows = c.rows, h = c.h0 + head;
-            const bool first = c.first, last = c.last, live = head < c.nh;
-            const float *src = c.src;
-            float *dst = c.dst;
-            uint32_t *flag = c.flag;
-            const float decay = c.decay[head], D = c.D[head];
+            // read again where it is needed: this chunk's is overwritten only after everyone
+            // has come to the next chunk's C B^T
+            const VarChunk &c = info[ph];
+            if (!ok || c.stop) break;
+            const int rows = c.rows;
+            const bool first = c.first, live = head < c.nh;
+            const float decay = c.decay[head];
             const int fac0 = c.factored[0], fac1 = c.factored[1];
             const float di0 = tabD[row], di1 = tabD[kVarQ + row];
             const float di = head ? di1 : di0;
-            const float eo = expf(di + c.total[head]);  // of Yo's row
             float w = tabW[head * kVarQ + row];
             if (!(head ? fac1 : fac0)) w *= expf(-di);
             if constexpr (SUMMARY) ssd_arrive(bEmpty);
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 float v[16];
                 if (!first) {
                     ssd_ld16(tS + col + q0, v);
-                } else if (src && live) {
+                } else if (const float *src = c.src; src && live) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] = __ldcg(src + (head * kSsdP + c0 + q0 + e) * kSsdN + row);
                 } else {
@@ -621,51 +623,47 @@ __global__ void __launch_bounds__(kVarThreads, 1)
 
             if constexpr (!SUMMARY) {
                 // C B^T with the decays of both heads, as bf16, over its own columns: this
-                // thread's 32 columns j of its row i
+                // thread's 32 columns j of its row i, 16 at a time
                 ok = __all_sync(0xffffffffu, ssd_wait(mG, ph, error));
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const int j0 = 64 * head + c0;
-                float v[32];
-                {
-                    float v0[16], v1[16];
-                    ssd_ld16(tG + lane_off + j0, v0);
-                    ssd_ld16(tG + lane_off + j0 + 16, v1);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {  // the causal mask, by selection: a zero whatever the later rows hold
-                        v[e] = j0 + e <= row ? v0[e] : 0.0f;
-                        v[16 + e] = j0 + 16 + e <= row ? v1[e] : 0.0f;
-                    }
-                }
+                for (int q0 = 0; q0 < 32; q0 += 16) {
+                    const int j0 = 64 * head + c0 + q0;
+                    float v[16];
+                    ssd_ld16(tG + lane_off + j0, v);
 #pragma unroll
-                for (int i = 0; i < kVarHeads; ++i) {
-                    const float4 *wj = reinterpret_cast<const float4 *>(tabW + i * kVarQ + j0);
-                    const float dr = i ? di1 : di0;
+                    for (int e = 0; e < 16; ++e)  // the causal mask, by selection: a zero whatever the later rows hold
+                        if (j0 + e > row) v[e] = 0.0f;
                     uint32_t r[16];
-                    if (i ? fac1 : fac0) {
-                        const float e = expf(dr);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 f = wj[k];
-                            r[2 * k] = pack_bf16x2(v[4 * k] * (e * f.x), v[4 * k + 1] * (e * f.y));
-                            r[2 * k + 1] = pack_bf16x2(v[4 * k + 2] * (e * f.z), v[4 * k + 3] * (e * f.w));
-                        }
-                    } else {
-                        // later rows (d smaller) would give factors above one, up to infinity:
-                        // their products are zeros by the mask, so the factor is capped there
-                        const float4 *dj = reinterpret_cast<const float4 *>(tabD + i * kVarQ + j0);
-                        auto factor = [&](float dc, float dtc, int j) {
-                            return j <= row ? ex2_approx((dr - dc) * kLog2e) * dtc : 0.0f;
-                        };
+                    for (int i = 0; i < kVarHeads; ++i) {
+                        const float4 *wj = reinterpret_cast<const float4 *>(tabW + i * kVarQ + j0);
+                        const float dr = i ? di1 : di0;
+                        if (i ? fac1 : fac0) {
+                            const float e = expf(dr);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 f = wj[k], dd = dj[k];
-                            const int j = j0 + 4 * k;
-                            r[2 * k] = pack_bf16x2(v[4 * k] * factor(dd.x, f.x, j), v[4 * k + 1] * factor(dd.y, f.y, j + 1));
-                            r[2 * k + 1] = pack_bf16x2(v[4 * k + 2] * factor(dd.z, f.z, j + 2), v[4 * k + 3] * factor(dd.w, f.w, j + 3));
+                            for (int k = 0; k < 4; ++k) {
+                                const float4 f = wj[k];
+                                r[8 * i + 2 * k] = pack_bf16x2(v[4 * k] * (e * f.x), v[4 * k + 1] * (e * f.y));
+                                r[8 * i + 2 * k + 1] = pack_bf16x2(v[4 * k + 2] * (e * f.z), v[4 * k + 3] * (e * f.w));
+                            }
+                        } else {
+                            // (the mask's columns may have factors up to infinity: left out too)
+                            const float4 *dj = reinterpret_cast<const float4 *>(tabD + i * kVarQ + j0);
+                            auto factor = [&](float dc, float dtc, int j) {
+                                return j <= row ? ex2_approx((dr - dc) * kLog2e) * dtc : 0.0f;
+                            };
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float4 f = wj[k], dd = dj[k];
+                                const int j = j0 + 4 * k;
+                                r[8 * i + 2 * k] = pack_bf16x2(v[4 * k] * factor(dd.x, f.x, j), v[4 * k + 1] * factor(dd.y, f.y, j + 1));
+                                r[8 * i + 2 * k + 1] = pack_bf16x2(v[4 * k + 2] * factor(dd.z, f.z, j + 2), v[4 * k + 3] * factor(dd.w, f.w, j + 3));
+                            }
                         }
                     }
-                    ssd_st16(tG + lane_off + j0 + 16 * i, r);
+                    ssd_st16(tG + lane_off + j0, r);
                 }
                 ssd_arrive(bEmpty);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -679,6 +677,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             if constexpr (!SUMMARY) {
                 // y = Yd + exp(d + T) Yo + D x, through this warp's part of the S tile (read by
                 // the products that are done) so that each store writes whole sectors
+                const float eo = expf(di + c.total[head]), D = c.D[head];
 #pragma unroll
                 for (int q0 = 0; q0 < 32; q0 += 16) {
                     float yd[16], yo[16];
@@ -696,7 +695,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 }
                 __syncwarp();
                 if (live) {
-                    uint16_t *yg = static_cast<uint16_t *>(p.y) + static_cast<int64_t>(t0) * p.y_stride + h * kSsdP;
+                    uint16_t *yg = static_cast<uint16_t *>(p.y) + static_cast<int64_t>(c.t0) * p.y_stride + (c.h0 + head) * kSsdP;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int r = quad * 32 + 8 * k + (lane >> 2), cc = c0 + 8 * (lane & 3);
@@ -708,7 +707,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 __syncwarp();  // the tile is S again in the next chunk
             }
             // the state after an item, and its hand-off once every thread's part is written
-            if (last && dst) {
+            if (float *dst = c.dst; c.last && dst) {
                 if (live) {
 #pragma unroll
                     for (int q0 = 0; q0 < 32; q0 += 16) {
@@ -718,12 +717,11 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                         for (int e = 0; e < 16; ++e) dst[(head * kSsdP + c0 + q0 + e) * kSsdN + row] = v[e];
                     }
                 }
-                if (flag) {
-                    __threadfence();
+                if (c.flag) {
                     ssd_arrive(bOut);
                     if (tid == 0 && ssd_wait(bOut, handed & 1u, error)) {
-                        __threadfence();
-                        st_release(flag, 1u);
+                        __threadfence();  // everyone's part, seen through the barrier, before the flag
+                        st_release(c.flag, 1u);
                     }
                     ++handed;
                     __syncwarp();

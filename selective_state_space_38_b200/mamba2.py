@@ -8,7 +8,6 @@ and workspaces that a call allocates belong to the stream the call runs on.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -70,18 +69,31 @@ def _rows(t, *, dtype=None, device=None, shape=None, name=""):
         raise TypeError(f"{name} must be a torch.Tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    size, strides = t.shape, t.stride()
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(shape)}")
     width = 1
-    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n > 1 and s != width:
-            raise ValueError(f"{name}: the elements of a row must lie together (strides {t.stride()})")
+    for i in range(len(size) - 1, 0, -1):
+        n = size[i]
+        if n > 1 and strides[i] != width:
+            raise ValueError(f"{name}: the elements of a row must lie together (strides {strides})")
         width *= n
-    if t.shape[0] > 1 and t.stride(0) < width:
-        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
-    return t.data_ptr(), max(t.stride(0) if t.shape[0] > 1 else width, width)
+    if size[0] <= 1:
+        return t.data_ptr(), width
+    if strides[0] < width:
+        raise ValueError(f"{name}: rows overlap (strides {strides})")
+    return t.data_ptr(), strides[0]
+
+
+def _flat(t, dtype, device, shape, name):
+    """Pointer of a contiguous tensor (None: no tensor); _ptr says what is wrong with others."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, dtype=dtype, device=device, shape=shape, name=name)
 
 
 def _cuda(x, rank, name):
@@ -96,27 +108,36 @@ def _cuda(x, rank, name):
     return x.device
 
 
-@contextlib.contextmanager
-def _on(device, stream):
+class _on:
     """The device and the stream of a call; what is allocated meanwhile belongs to that stream."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+    __slots__ = ("device", "stream", "inside")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.inside = device, stream, ()
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self.inside += (torch.cuda.device(self.device),)
+        if self.stream is not None:
+            self.inside += (torch.cuda.stream(self.stream),)
+        for c in self.inside:
+            c.__enter__()
+        return (self.stream or torch.cuda.current_stream(self.device)).cuda_stream
+
+    def __exit__(self, *error):
+        for c in reversed(self.inside):
+            c.__exit__(*error)
 
 
 def _tables(cu_seqlens, slots, has_initial, device):
     """Pointers of the packed sequences' tables, and the number of sequences."""
-    pc = _ptr(cu_seqlens, dtype=torch.int32, device=device, name="cu_seqlens")
-    if pc is None or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must be [sequences + 1]")
-    n = cu_seqlens.numel() - 1
-    ps = _ptr(slots, dtype=torch.int32, device=device, shape=(n,), name="slots")
-    if has_initial is not None and has_initial.dtype != torch.uint8:
-        _ptr(has_initial, dtype=torch.bool, device=device, name="has_initial")
-    ph = _ptr(has_initial, device=device, shape=(n,), name="has_initial")
+    n = cu_seqlens.shape[0] - 1
+    pc = _flat(cu_seqlens, torch.int32, device, (n + 1,), "cu_seqlens")
+    ps = _flat(slots, torch.int32, device, (n,), "slots")
+    ph = _flat(has_initial, torch.uint8 if has_initial is not None and has_initial.dtype is torch.uint8 else torch.bool, device,
+               (n,), "has_initial")
     return pc, ps, ph, n
 
 
@@ -144,13 +165,13 @@ def ssm_conv1d_fwd(x, conv_w, conv_bias, cu_seqlens, windows=None, slots=None, h
     code = _act_code(x)
     K = int(conv_w.shape[1])
     px, xs = _rows(x, device=dev, name="x")
-    pw = _ptr(conv_w, dtype=f32, device=dev, shape=(dim, K), name="conv_w")
-    pb = _ptr(conv_bias, dtype=f32, device=dev, shape=(dim,), name="conv_bias")
+    pw = _flat(conv_w, f32, dev, (dim, K), "conv_w")
+    pb = _flat(conv_bias, f32, dev, (dim,), "conv_bias")
     pc, ps, ph, n = _tables(cu_seqlens, slots, has_initial, dev)
     nslots = 0
     if windows is not None:
         nslots = windows.shape[0]
-    pwin = _ptr(windows, dtype=act, device=dev, shape=(nslots, K - 1, dim), name="windows")
+    pwin = _flat(windows, act, dev, (nslots, K - 1, dim), "windows")
     with _on(dev, stream) as sp:
         if out is None:
             out = torch.empty((T, dim), dtype=act, device=dev)
@@ -171,11 +192,11 @@ def ssm_conv1d_step(windows, x, conv_w, conv_bias, slots=None, silu=True, out=No
     code = _act_code(x)
     K = int(conv_w.shape[1])
     px, xs = _rows(x, device=dev, name="x")
-    pw = _ptr(conv_w, dtype=f32, device=dev, shape=(dim, K), name="conv_w")
-    pb = _ptr(conv_bias, dtype=f32, device=dev, shape=(dim,), name="conv_bias")
-    ps = _ptr(slots, dtype=torch.int32, device=dev, shape=(b,), name="slots")
+    pw = _flat(conv_w, f32, dev, (dim, K), "conv_w")
+    pb = _flat(conv_bias, f32, dev, (dim,), "conv_bias")
+    ps = _flat(slots, torch.int32, dev, (b,), "slots")
     nslots = windows.shape[0] if windows is not None else b
-    pwin = _ptr(windows, dtype=act, device=dev, shape=(nslots, K - 1, dim), name="windows")
+    pwin = _flat(windows, act, dev, (nslots, K - 1, dim), "windows")
     with _on(dev, stream) as sp:
         if out is None:
             out = torch.empty((b, dim), dtype=act, device=dev)
@@ -195,8 +216,8 @@ def ssm_conv1d_bwd(x, conv_w, conv_bias, cu_seqlens, dy, silu=True, dx=None, str
     code = _act_code(x)
     K = int(conv_w.shape[1])
     px, xs = _rows(x, device=dev, name="x")
-    pw = _ptr(conv_w, dtype=f32, device=dev, shape=(dim, K), name="conv_w")
-    pb = _ptr(conv_bias, dtype=f32, device=dev, shape=(dim,), name="conv_bias")
+    pw = _flat(conv_w, f32, dev, (dim, K), "conv_w")
+    pb = _flat(conv_bias, f32, dev, (dim,), "conv_bias")
     pc, _, _, n = _tables(cu_seqlens, None, None, dev)
     pdy, dys = _rows(dy, dtype=act, device=dev, shape=(T, dim), name="dy")
     with _on(dev, stream) as sp:
@@ -225,9 +246,9 @@ def _ssd_args(x, dt, dt_bias, A, B, C, D, dev):
     pdt, dts = _rows(dt, dtype=act, device=dev, shape=(T, H), name="dt")
     pB, bs = _rows(B, dtype=act, device=dev, shape=(T, G, N), name="B")
     pC, cs = _rows(C, dtype=act, device=dev, shape=(T, G, N), name="C")
-    pbias = _ptr(dt_bias, dtype=f32, device=dev, shape=(H,), name="dt_bias")
-    pA = _ptr(A, dtype=f32, device=dev, shape=(H,), name="A")
-    pD = _ptr(D, dtype=f32, device=dev, shape=(H,), name="D")
+    pbias = _flat(dt_bias, f32, dev, (H,), "dt_bias")
+    pA = _flat(A, f32, dev, (H,), "A")
+    pD = _flat(D, f32, dev, (H,), "D")
     dims = SsdPackedDims(T, 0, 0, H, P, G, N, xs, dts, bs, cs, 0, _act_code(x))
     return px, pdt, pbias, pA, pB, pC, pD, dims
 
@@ -248,8 +269,7 @@ def ssm_ssd_varlen_fwd(x, dt, dt_bias, softplus, A, B, C, D, cu_seqlens, states=
     pc, ps, ph, n = _tables(cu_seqlens, slots, has_initial, dev)
     dims.sequences = n
     dims.slots = states.shape[0] if states is not None else 0
-    pst = _ptr(states, dtype=torch.float32, device=dev, shape=(dims.slots, dims.heads, dims.headdim, dims.dstate),
-               name="states")
+    pst = _flat(states, torch.float32, dev, (dims.slots, dims.heads, dims.headdim, dims.dstate), "states")
     lib = get_lib()
     with _on(dev, stream) as sp:
         if out is None:
@@ -274,9 +294,8 @@ def ssm_ssd_step(states, x, dt, dt_bias, softplus, A, B, C, D=None, slots=None, 
     if not isinstance(states, torch.Tensor):
         raise TypeError("states must be a torch.Tensor")
     dims.slots = states.shape[0]
-    pst = _ptr(states, dtype=torch.float32, device=dev, shape=(dims.slots, dims.heads, dims.headdim, dims.dstate),
-               name="states")
-    ps = _ptr(slots, dtype=torch.int32, device=dev, shape=(x.shape[0],), name="slots")
+    pst = _flat(states, torch.float32, dev, (dims.slots, dims.heads, dims.headdim, dims.dstate), "states")
+    ps = _flat(slots, torch.int32, dev, (x.shape[0],), "slots")
     with _on(dev, stream) as sp:
         if out is None:
             out = torch.empty(tuple(x.shape), dtype=x.dtype, device=dev)
@@ -291,7 +310,7 @@ def _norm_args(x, weight, z, groups, eps, gate_first):
     rows, dim = x.shape
     px, xs = _rows(x, device=dev, name="x")
     pz, zs = _rows(z, dtype=x.dtype, device=dev, shape=x.shape, name="z")
-    pw = _ptr(weight, dtype=torch.float32, device=dev, shape=(dim,), name="weight")
+    pw = _flat(weight, torch.float32, dev, (dim,), "weight")
     dims = NormDims(rows, dim, int(groups), xs, zs, 0, 0, 0, 0, float(eps), int(bool(gate_first)), _act_code(x))
     return dev, px, pz, pw, dims
 
