@@ -41,41 +41,48 @@ constexpr int kConvThreads = 128;
 constexpr int kConvBatch = 8;   // rows loaded ahead
 constexpr int kConvBwdBatch = 4;
 
-// The sequences of a block's tile.  All its rows are walked by every thread of the
-// block in step, so the current sequence is the block's; the first 32 from the
-// tile's start wait in shared memory, since each would cost dependent loads.
+// The sequences of a block's tile, rows counted from the tile's first (32 bits).  All
+// rows are walked by every thread of the block in step, so the current sequence is
+// the block's; the first 32 from the tile's start wait in shared memory, since each
+// would cost dependent loads.
 struct ConvWalk {
-    int n;               // the current sequence (`sequences`: none any more)
-    int64_t start, end;  // its rows
-    int slot;            // the window it goes on from, or -1
-    const int64_t *ends;
-    const int *slots;
+    int n;           // the current sequence (`sequences`: none any more)
+    int start, end;  // its rows
+    int slot;        // the window it goes on from, or -1
+    const int *ends, *slots;
     int base;
+    int64_t t0;
 
-    __device__ __forceinline__ static void stage(const Conv1dParams &p, int base, int64_t *ends, int *slots) {
-        const int i = threadIdx.x;
-        if (i < 32) {
-            const int n = base + i;
-            const bool in = n < p.seq.sequences;
-            ends[i] = in ? packed_at(p.seq, n + 1) : 0;
-            slots[i] = in && p.windows && p.seq.has_initial && p.seq.has_initial[n] ? packed_slot(p.seq, n) : -1;
+    __device__ __forceinline__ int rel(int64_t t) const {
+        const int64_t d = t - t0;
+        return static_cast<int>(d < -(1 << 30) ? -(1 << 30) : d > (1 << 30) ? (1 << 30) : d);
+    }
+    __device__ __forceinline__ void stage(const Conv1dParams &p, int64_t first, int *e, int *s) {
+        t0 = first, ends = e, slots = s;
+        n = base = packed_find(p.seq, t0);
+        start = 0, end = -1, slot = -1;
+        if (threadIdx.x < 32) {
+            const int i = threadIdx.x, m = base + i;
+            const bool in = m < p.seq.sequences;
+            e[i] = in ? rel(packed_at(p.seq, m + 1)) : 0;
+            s[i] = in && p.windows && p.seq.has_initial && p.seq.has_initial[m] ? packed_slot(p.seq, m) : -1;
         }
         __syncthreads();
     }
     __device__ __forceinline__ void enter(const Conv1dParams &p) {  // sequence n
         const int i = n - base;
         if (i < 32) {
-            start = i > 0 ? ends[i - 1] : packed_at(p.seq, n);
+            start = i > 0 ? ends[i - 1] : rel(packed_at(p.seq, n));
             end = ends[i];
             slot = slots[i];
         } else {
-            start = packed_at(p.seq, n);
-            end = packed_at(p.seq, n + 1);
+            start = rel(packed_at(p.seq, n));
+            end = rel(packed_at(p.seq, n + 1));
             slot = p.windows && p.seq.has_initial && p.seq.has_initial[n] ? packed_slot(p.seq, n) : -1;
         }
     }
-    // on to the sequence that row t is in; false: behind the last one
-    __device__ __forceinline__ bool to(const Conv1dParams &p, int64_t t) {
+    // on to the sequence that row r is in; false: behind the last one
+    __device__ __forceinline__ bool to(const Conv1dParams &p, int r) {
         do {
             if (n + 1 >= p.seq.sequences) {
                 n = p.seq.sequences;
@@ -83,7 +90,7 @@ struct ConvWalk {
             }
             ++n;
             enter(p);
-        } while (t >= end);
+        } while (r >= end);
         return true;
     }
 };
@@ -111,14 +118,14 @@ struct ConvChannels {
             b[i] = Lanes<kL>::of(g[i * kL], g[i * kL + kL - 1]);
         }
     }
-    // The inputs before row t of the current sequence: its rows, before its first the
+    // The inputs before row `at` of the current sequence: its rows, before its first the
     // window it goes on from, else zeros.
-    __device__ __forceinline__ void history(const Conv1dParams &p, const ConvWalk &q, int64_t t, int64_t c) {
-        const int64_t pos = t > q.start ? t - q.start : 0;
+    __device__ __forceinline__ void history(const Conv1dParams &p, const ConvWalk &q, int at, int64_t c) {
+        const int pos = max(at - q.start, 0);
 #pragma unroll
         for (int d = 0; d < K - 1; ++d) {
             typename R::Raw r = R::zero_raw();
-            if (pos - d - 1 >= 0) r = R::load_raw(p.x, (t - d - 1) * p.x_stride + c);
+            if (pos - d - 1 >= 0) r = R::load_raw(p.x, (q.t0 + at - d - 1) * p.x_stride + c);
             else if (q.slot >= 0) r = R::load_raw(p.windows, (static_cast<int64_t>(q.slot) * (K - 1) + (K - 1 + pos - d - 1)) * p.dim + c);
 #pragma unroll
             for (int i = 0; i < kN; ++i) h[d][i] = R::pair(r, i);
@@ -144,57 +151,64 @@ __global__ void __launch_bounds__(kConvThreads) conv1d_fwd_kernel(const Conv1dPa
     using R = Row<T, V>;
     constexpr bool kAccurate = Act<T>::kBytes == 4;
     constexpr int kL = R::kL, kN = R::kN;
-    __shared__ int64_t ends[32];
-    __shared__ int slots[32];
+    __shared__ int ends[32], slots[32];
     const int64_t t0 = static_cast<int64_t>(blockIdx.x / p.cblocks) * p.tile;
-    const int64_t t1 = min(t0 + p.tile, p.seq.tokens);
+    const int rows = static_cast<int>(min(p.tile, p.seq.tokens - t0));
     ConvWalk q;
-    q.n = q.base = packed_find(p.seq, t0);
-    q.ends = ends, q.slots = slots;
-    if (q.n >= p.seq.sequences) return;
-    ConvWalk::stage(p, q.base, ends, slots);
+    q.stage(p, t0, ends, slots);
     const int64_t c = (static_cast<int64_t>(blockIdx.x % p.cblocks) * kConvThreads + threadIdx.x) * V;
-    if (c >= p.dim) return;
+    if (q.n >= p.seq.sequences || c >= p.dim) return;
+    // the rows' bytes from the tile's first
+    const char *x = static_cast<const char *>(p.x) + (t0 * p.x_stride + c) * Act<T>::kBytes;
+    char *y = static_cast<char *>(p.y) + (t0 * p.y_stride + c) * Act<T>::kBytes;
+    const int64_t xs = p.x_stride * Act<T>::kBytes, ys = p.y_stride * Act<T>::kBytes;
     ConvChannels<T, V, K> ch;
     typename R::Raw raw[kConvBatch];
-    auto load = [&](int64_t t) {
+    auto load = [&](int r) {  // rows r, r + 1, ...: `x` is row r's
+        if (r + kConvBatch <= rows) {
 #pragma unroll
-        for (int i = 0; i < kConvBatch; ++i)
-            if (t + i < t1) raw[i] = R::load_raw(p.x, (t + i) * p.x_stride + c);
+            for (int i = 0; i < kConvBatch; ++i) raw[i] = R::load_raw(x + i * xs, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kConvBatch; ++i)
+                if (r + i < rows) raw[i] = R::load_raw(x + i * xs, 0);
+        }
+        x += kConvBatch * xs;
     };
-    load(t0);
+    load(0);
     q.enter(p);
     ch.taps(p, c);
-    ch.history(p, q, t0, c);
-    auto row = [&](int64_t t, const typename R::Raw &r) {
-        Lanes<kL> x[kN], u[kN];
+    ch.history(p, q, 0, c);
+    auto row = [&](const typename R::Raw &r) {  // `y` is its row
+        Lanes<kL> v[kN], u[kN];
 #pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] = R::pair(r, i);
-        ch.row(x, u);
+        for (int i = 0; i < kN; ++i) v[i] = R::pair(r, i);
+        ch.row(v, u);
         if (p.silu) {
 #pragma unroll
             for (int i = 0; i < kN; ++i) u[i] = u[i] * sigmoid_lanes<kAccurate, kL>(u[i]);
         }
-        R::store(p.y, t * p.y_stride + c, u);
+        R::store(y, 0, u);
+        y += ys;
     };
-    for (int64_t t = t0; t < t1; t += kConvBatch) {
+    for (int r = 0; r < rows; r += kConvBatch) {
         typename R::Raw now[kConvBatch];
 #pragma unroll
         for (int i = 0; i < kConvBatch; ++i) now[i] = raw[i];
-        load(t + kConvBatch);
-        if (t + kConvBatch <= min(t1, q.end)) {  // rows of one sequence: the history's moves are renamings
+        load(r + kConvBatch);
+        if (r + kConvBatch <= min(rows, q.end)) {  // rows of one sequence: the history's moves are renamings
 #pragma unroll
-            for (int i = 0; i < kConvBatch; ++i) row(t + i, now[i]);
+            for (int i = 0; i < kConvBatch; ++i) row(now[i]);
             continue;
         }
 #pragma unroll
         for (int i = 0; i < kConvBatch; ++i) {
-            if (t + i >= t1) break;
-            if (t + i >= q.end) {
-                if (!q.to(p, t + i)) return;  // rows behind the last sequence stay as they were
-                ch.history(p, q, t + i, c);
+            if (r + i >= rows) break;
+            if (r + i >= q.end) {
+                if (!q.to(p, r + i)) return;  // rows behind the last sequence stay as they were
+                ch.history(p, q, r + i, c);
             }
-            row(t + i, now[i]);
+            row(now[i]);
         }
     }
 }
@@ -276,20 +290,16 @@ __global__ void __launch_bounds__(kConvThreads) conv1d_bwd_kernel(const Conv1dPa
     constexpr bool kAccurate = Act<T>::kBytes == 4;
     constexpr int kL = R::kL, kN = R::kN, kB = kConvBwdBatch;
     using Ln = Lanes<kL>;
-    __shared__ int64_t ends[32];
-    __shared__ int slots[32];
+    __shared__ int ends[32], slots[32];
     const int64_t t0 = static_cast<int64_t>(blockIdx.x / p.cblocks) * p.tile;
-    const int64_t t1 = min(t0 + p.tile, p.seq.tokens);
+    const int rows = static_cast<int>(min(p.tile, p.seq.tokens - t0));
     ConvWalk q;
-    q.n = q.base = packed_find(p.seq, t0);
-    q.ends = ends, q.slots = slots;
-    q.start = 0, q.end = -1, q.slot = -1;
-    ConvWalk::stage(p, q.base, ends, slots);
+    q.stage(p, t0, ends, slots);
     const int64_t c = (static_cast<int64_t>(blockIdx.x % p.cblocks) * kConvThreads + threadIdx.x) * V;
     if (c >= p.dim) return;
     ConvChannels<T, V, K> ch;
     Ln g[K][kN], dw[K][kN], db[kN];
-    int64_t eh[K];
+    int eh[K];
 #pragma unroll
     for (int d = 0; d < K; ++d) {
         eh[d] = -1;
@@ -298,21 +308,29 @@ __global__ void __launch_bounds__(kConvThreads) conv1d_bwd_kernel(const Conv1dPa
     }
 #pragma unroll
     for (int i = 0; i < kN; ++i) db[i] = lanes<kL>(0.0f);
-    const int64_t last = t1 + K - 1;  // the rows after the tile complete its last gradients
+    // the rows after the tile complete its last gradients; there may be fewer of them
+    const int last = rows + K - 1, have = static_cast<int>(min(static_cast<int64_t>(last), p.seq.tokens - t0));
+    const char *x = static_cast<const char *>(p.x) + (t0 * p.x_stride + c) * Act<T>::kBytes;
+    const char *dy = static_cast<const char *>(p.dy) + (t0 * p.dy_stride + c) * Act<T>::kBytes;
+    char *dx = static_cast<char *>(p.dx) + ((t0 - (K - 1)) * p.dx_stride + c) * Act<T>::kBytes;  // of the row whose gradient is complete
+    const int64_t xs = p.x_stride * Act<T>::kBytes, dys = p.dy_stride * Act<T>::kBytes, dxs = p.dx_stride * Act<T>::kBytes;
     typename R::Raw rx[kB], rd[kB];
-    auto load = [&](int64_t t) {
+    auto load = [&](int r) {  // rows r, r + 1, ...: `x` and `dy` are row r's
+        if (r + kB <= have) {
 #pragma unroll
-        for (int i = 0; i < kB; ++i) {
-            if (t + i >= last || t + i >= p.seq.tokens) continue;
-            rx[i] = R::load_raw(p.x, (t + i) * p.x_stride + c);
-            rd[i] = R::load_raw(p.dy, (t + i) * p.dy_stride + c);
+            for (int i = 0; i < kB; ++i) rx[i] = R::load_raw(x + i * xs, 0), rd[i] = R::load_raw(dy + i * dys, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kB; ++i)
+                if (r + i < have) rx[i] = R::load_raw(x + i * xs, 0), rd[i] = R::load_raw(dy + i * dys, 0);
         }
+        x += kB * xs, dy += kB * dys;
     };
-    load(t0);
+    load(0);
     ch.taps(p, c);
     if (q.n < p.seq.sequences) {
         q.enter(p);
-        ch.history(p, q, t0, c);
+        ch.history(p, q, 0, c);
     }
     // g of a row that is in a sequence, and its part of the sums
     auto row = [&](const typename R::Raw &rxi, const typename R::Raw &rdi, bool count) {
@@ -343,40 +361,41 @@ __global__ void __launch_bounds__(kConvThreads) conv1d_bwd_kernel(const Conv1dPa
             }
         }
     };
-    for (int64_t t = t0; t < last; t += kB) {
+    for (int r = 0; r < last; r += kB) {
         typename R::Raw nx[kB], nd[kB];
 #pragma unroll
         for (int i = 0; i < kB; ++i) nx[i] = rx[i], nd[i] = rd[i];
-        load(t + kB);
+        load(r + kB);
         // rows of one sequence whose K - 1 rows before are the same sequence's and the tile's
-        if (t - (K - 1) >= max(t0, q.start) && t + kB <= min(t1, q.end)) {
+        if (r - (K - 1) >= max(0, q.start) && r + kB <= min(rows, q.end)) {
 #pragma unroll
-            for (int r = 0; r < kB; ++r) {
-                row(nx[r], nd[r], true);
-                Ln dx[kN];
+            for (int e = 0; e < kB; ++e) {
+                row(nx[e], nd[e], true);
+                Ln v[kN];
 #pragma unroll
                 for (int i = 0; i < kN; ++i) {
-                    dx[i] = ch.w[0][i] * g[0][i];
+                    v[i] = ch.w[0][i] * g[0][i];
 #pragma unroll
-                    for (int d = 1; d < K; ++d) dx[i] = Ln::fma(ch.w[d][i], g[d][i], dx[i]);
+                    for (int d = 1; d < K; ++d) v[i] = Ln::fma(ch.w[d][i], g[d][i], v[i]);
                 }
-                R::store(p.dx, (t + r - (K - 1)) * p.dx_stride + c, dx);
+                R::store(dx, 0, v);
+                dx += dxs;
             }
 #pragma unroll
             for (int d = 0; d < K; ++d) eh[d] = q.end;
             continue;
         }
 #pragma unroll
-        for (int r = 0; r < kB; ++r) {
-            const int64_t s = t + r;
+        for (int e = 0; e < kB; ++e) {
+            const int s = r + e;
             if (s >= last) break;
             if (q.n < p.seq.sequences && s >= q.end && q.to(p, s)) ch.history(p, q, s, c);
-            const bool live = q.n < p.seq.sequences && s < p.seq.tokens;
+            const bool live = q.n < p.seq.sequences && s < have;
 #pragma unroll
             for (int d = K - 1; d > 0; --d) eh[d] = eh[d - 1];
             eh[0] = live ? q.end : -1;
             if (live) {
-                row(nx[r], nd[r], s < t1);
+                row(nx[e], nd[e], s < rows);
             } else {
 #pragma unroll
                 for (int i = 0; i < kN; ++i) {
@@ -385,19 +404,19 @@ __global__ void __launch_bounds__(kConvThreads) conv1d_bwd_kernel(const Conv1dPa
                     g[0][i] = lanes<kL>(0.0f);
                 }
             }
-            const int64_t done = s - (K - 1);  // the row whose gradient is complete
-            if (done >= t0 && eh[K - 1] >= 0) {
-                Ln dx[kN];
+            if (s >= K - 1 && eh[K - 1] >= 0) {  // the row s - (K - 1), when it is in a sequence
+                Ln v[kN];
 #pragma unroll
-                for (int i = 0; i < kN; ++i) dx[i] = lanes<kL>(0.0f);
+                for (int i = 0; i < kN; ++i) v[i] = lanes<kL>(0.0f);
 #pragma unroll
-                for (int d = 0; d < K; ++d)  // g[d] is row s - d = done + (K - 1 - d): its tap on that row is d
+                for (int d = 0; d < K; ++d)  // g[d] is row s - d: its tap on row s - (K - 1) is d
                     if (s - d < eh[K - 1]) {
 #pragma unroll
-                        for (int i = 0; i < kN; ++i) dx[i] = Ln::fma(ch.w[d][i], g[d][i], dx[i]);
+                        for (int i = 0; i < kN; ++i) v[i] = Ln::fma(ch.w[d][i], g[d][i], v[i]);
                     }
-                R::store(p.dx, done * p.dx_stride + c, dx);
+                R::store(dx, 0, v);
             }
+            dx += dxs;
         }
     }
     float *o = p.partial + static_cast<int64_t>(blockIdx.x / p.cblocks) * (K + 1) * p.dim + c;
