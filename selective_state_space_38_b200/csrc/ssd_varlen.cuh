@@ -31,10 +31,12 @@
 // Per pair of heads and chunk: 96 KB loaded through TMA and six products of
 // 128 x 128 x 128, 3072 cycles of the tensor pipe at 8192 bf16 flops a cycle;
 // shared memory carries about 670 KB for them and their operands, 5200 cycles at
-// 128 bytes a cycle, which bounds the chunk.  One CTA per SM: a producer warp
-// issues every TMA load and MMA, a table warp walks the work list a chunk ahead
-// (running sums and factors), and sixteen epilogue warps scale, mask and store.
-// Every wait is bounded.
+// 128 bytes a cycle, which bounds the chunk.  One CTA per SM: one warp issues the
+// TMA loads and one the MMAs, a table warp walks the work list a chunk ahead
+// (running sums and factors), and sixteen epilogue warps work in two halves: eight
+// on the state (S and its operand, the parts of x), eight on the output (C B^T with
+// its decays, y), so that a chunk's y is written while the next one's state and
+// operands are formed.  Every wait is bounded.
 //
 // Long sequences are cut into segments.  Chained, a segment waits for the state of
 // the one before; where that would leave SMs idle (few heads, long sequences) the
@@ -54,8 +56,8 @@ constexpr int kVarQ = 128;          // steps of a chunk at most
 constexpr int kVarSegment = 1024;   // tokens of a work item at least (all but a sequence's last)
 constexpr int kVarMaxWindows = 1024;
 constexpr float kVarRange = 80.0f;
-constexpr int kVarEpilogue = 512;
-constexpr int kVarThreads = kVarEpilogue + 64;  // + the producer warp and the table warp
+constexpr int kVarHalf = 256;       // epilogue threads on the state, and on the output
+constexpr int kVarThreads = 2 * kVarHalf + 96;  // + a warp for the MMAs, the loads and the tables each
 constexpr int kVarHeads = 2;        // heads walked together
 constexpr int kVarParts = 3;        // bf16 parts of exp(-d) dt x
 
@@ -215,12 +217,13 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     float *tabD = reinterpret_cast<float *>(sm + S::kTabD), *tabW = reinterpret_cast<float *>(sm + S::kTabW);
     VarChunk *info = reinterpret_cast<VarChunk *>(sm + S::kInfo);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + S::kBar);
-    uint64_t *bFull = bar, *bX = bar + 1, *bCB = bar + 2;          // tables and info written; X landed; C and B landed
-    uint64_t *mG = bar + 3, *mY = bar + 4;                         // C B^T; every product of the chunk done
-    uint64_t *bEmpty = bar + 5;                                    // info read by everyone, tables done with
-    uint64_t *bS = bar + 6, *bE1 = bar + 7, *bE2 = bar + 8;        // S; the parts of x; C B^T with its decays written
-    uint64_t *bOut = bar + 9;                                      // a handed-on state written
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 10);
+    uint64_t *bFull = bar, *bX = bar + 1;                          // tables and info written; X landed
+    uint64_t *mG = bar + 2, *mC = bar + 3, *mS = bar + 4, *mY = bar + 5;  // C B^T; C S; the state; Yd done
+    uint64_t *bCB = bar + 6;                                       // C and B landed
+    uint64_t *bEmpty = bar + 7;                                    // info read by everyone, tables done with
+    uint64_t *bS = bar + 8, *bE1 = bar + 9, *bOut = bar + 10;      // S; the parts of x; a handed-on state written
+    uint64_t *bE2 = bar + 11, *bYf = bar + 12;                     // C B^T with its decays written; y out of the S tile
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 13);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t *error = p.work.error;
 
@@ -233,8 +236,8 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     const bool parallel = *reinterpret_cast<volatile uint32_t *>(p.work.parallel) != 0;
     if (SUMMARY && !parallel) return;
     if (tid == 0) {
-        for (int i = 0; i < 10; ++i) {
-            const uint32_t n = i == 5 ? kVarEpilogue + 1 : i > 5 ? kVarEpilogue : 1;
+        for (int i = 0; i < 13; ++i) {
+            const uint32_t n = i == 7 ? (SUMMARY ? 1 : 2) * kVarHalf + 2 : i > 7 ? kVarHalf : i == 6 && !SUMMARY ? 2 : 1;
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar + i)), "r"(n));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -253,107 +256,158 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     const uint32_t tG = tbase, tYd = tbase + 128, tYo = tbase + 256, tS = tbase + 384;
     constexpr int kN = 64 * kVarHeads;
 
-    if (warp == kVarEpilogue / 32) {
-        // ---- producer: one lane issues the loads and the products --------------------
-        if (lane == 0) {
-            const uint32_t aC = smem_u32(sm + S::kC), aB = smem_u32(sm + S::kB), aX = smem_u32(sm + S::kX),
-                           aXp = smem_u32(sm + S::kXp), aS = smem_u32(sm + S::kS);
-            uint32_t nL = 0, wL = 0, nG = 0, nY = 0, wY = 0;  // issued, waited for
-            int t0 = 0, h0 = 0, nh = 0, g = 0;
-            auto next = [&](uint32_t u) -> bool {  // the chunk's numbers; false: no more
-                if (!ssd_wait(bFull, u & 1u, error)) return false;
-                const VarChunk &c = info[u & 1u];
-                const bool go = !c.stop;
-                t0 = c.t0, h0 = c.h0, nh = c.nh, g = c.g;
-                ssd_arrive(bEmpty);
-                return go;
-            };
-            auto load = [&]() {
-                mbar_arrive_expect_tx(bX, nh * S::kTile);
-                for (int i = 0; i < nh; ++i) tma_load_3d(sm + S::kX + i * S::kTile, &tm.x, 0, h0 + i, t0, bX);
-                mbar_arrive_expect_tx(bCB, (SUMMARY ? 2 : 4) * S::kTile);
-                tma_load_3d(sm + S::kB, &tm.B, 0, g, t0, bCB);
-                tma_load_3d(sm + S::kB + S::kTile, &tm.B, 64, g, t0, bCB);
-                if constexpr (!SUMMARY) {
-                    tma_load_3d(sm + S::kC, &tm.C, 0, g, t0, bCB);
-                    tma_load_3d(sm + S::kC + S::kTile, &tm.C, 64, g, t0, bCB);
+    // The waits of the two issuing warps, which stay converged: a bounded one, and a test.
+    auto wait = [&](uint64_t *b, uint32_t ph) -> bool { return __all_sync(0xffffffffu, ssd_wait(b, ph, error)); };
+    auto test = [&](uint64_t *b, uint32_t ph) -> bool { return __any_sync(0xffffffffu, ssd_try(smem_u32(b), ph)); };
+    auto give_up = [&](uint32_t n) -> bool {  // after n tests in vain
+        if (n >= kSsdWaitLimit && lane == 0) atomicOr(error, 2u);
+        return n >= kSsdWaitLimit || ((n & 1023u) == 1023u && __any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(error) != 0));
+    };
+    if (warp == 2 * kVarHalf / 32) {
+        // ---- the products, issued by one elected lane -----------------------------------
+        const uint32_t aC = smem_u32(sm + S::kC), aB = smem_u32(sm + S::kB), aX = smem_u32(sm + S::kX),
+                       aXp = smem_u32(sm + S::kXp), aS = smem_u32(sm + S::kS);
+        uint32_t nG = 0, nC = 0, nS = 0, nY = 0;  // issued
+        for (uint32_t u = 0;; ++u) {
+            const uint32_t ph = u & 1u;
+            if (!wait(bFull, ph)) break;
+            const int heads = info[ph].nh;
+            const bool stop = info[ph].stop;
+            __syncwarp();
+            if (lane == 0) ssd_arrive(bEmpty);
+            // (Yd before has read what C B^T replaces: mY)
+            if (stop || !wait(bCB, ph) || (!SUMMARY && u > 0 && !wait(mY, ph ^ 1u))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if constexpr (!SUMMARY) {
+                if (ssd_elect()) {  // C B^T
+                    constexpr uint32_t id = ssd_idesc(128, 128, 0, 0);
+                    const uint64_t dC = ssd_desc(aC, 16, 1024), dB = ssd_desc(aB, 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t o = ((k / 4) * S::kTile + (k % 4) * 32) >> 4;
+                        ssd_mma(tG, dC + o, dB + o, id, k > 0);
+                    }
+                    ssd_commit(mG);
                 }
-                ++nL;
-            };
-            bool go = next(0);
-            if (go) load();
-            for (uint32_t u = 0; go; ++u) {
-                const uint32_t ph = u & 1u;
-                if (!ssd_wait(bCB, ph, error)) break;
+                __syncwarp();
+                nG = u + 1;
+                if (!wait(bS, ph)) break;  // (S is written after the y before was read)
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                if constexpr (!SUMMARY) {
-                    {   // C B^T
-                        constexpr uint32_t id = ssd_idesc(128, 128, 0, 0);
-                        const uint64_t dC = ssd_desc(aC, 16, 1024), dB = ssd_desc(aB, 16, 1024);
+                if (ssd_elect()) {  // Yo = C S
+                    constexpr uint32_t id = ssd_idesc(128, kN, 0, 1);
+                    const uint64_t dC = ssd_desc(aC, 16, 1024), dS = ssd_desc(aS, S::kTile, 1024);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t o = ((k / 4) * S::kTile + (k % 4) * 32) >> 4;
-                            ssd_mma(tG, dC + o, dB + o, id, k > 0);
-                        }
-                        ssd_commit(mG);
-                        nG = u + 1;
-                    }
-                    if (!ssd_wait(bS, ph, error)) break;
-                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    {   // Yo = C S
-                        constexpr uint32_t id = ssd_idesc(128, kN, 0, 1);
-                        const uint64_t dC = ssd_desc(aC, 16, 1024), dS = ssd_desc(aS, S::kTile, 1024);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            ssd_mma(tYo, dC + (((k / 4) * S::kTile + (k % 4) * 32) >> 4), dS + ((2048 * k) >> 4), id, k > 0);
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        ssd_mma(tYo, dC + (((k / 4) * S::kTile + (k % 4) * 32) >> 4), dS + ((2048 * k) >> 4), id, k > 0);
+                    ssd_commit(mC);
                 }
-                const bool parts = ssd_wait(bE1, ph, error);
-                if (parts) {  // S += B^T (exp(-d) dt x), the smallest part first
-                    wL = u + 1;  // the epilogue warps read X before they arrived
+                __syncwarp();
+                nC = u + 1;
+            }
+            // the state's products and Yd, whichever has its operands first
+            bool state = false, yd = SUMMARY;
+            for (uint32_t n = 0; !(state && yd) && !give_up(n); ++n) {
+                if (!state && test(bE1, ph)) {
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    constexpr uint32_t id = ssd_idesc(128, kN, 1, 1);
-                    const uint64_t dB = ssd_desc(aB, S::kTile, 1024);
+                    if (ssd_elect()) {  // S += B^T (exp(-d) dt x), the smallest part first
+                        constexpr uint32_t id = ssd_idesc(128, kN, 1, 1);
+                        const uint64_t dB = ssd_desc(aB, S::kTile, 1024), dX = ssd_desc(aXp, S::kTile, 1024);
 #pragma unroll
-                    for (int part = kVarParts - 1; part >= 0; --part) {
-                        const uint64_t dX = ssd_desc(aXp + part * kVarHeads * S::kTile, S::kTile, 1024);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            ssd_mma(tS, dB + ((2048 * k) >> 4), dX + ((2048 * k) >> 4), id, 1);
-                    }
-                }
-                bool decays = parts;
-                if constexpr (!SUMMARY) {
-                    decays = parts && ssd_wait(bE2, ph, error);
-                    if (decays) {  // Yd = (C B^T with its decays) x, per head
-                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        constexpr uint32_t id = ssd_idesc(128, 64, 0, 1);
-                        for (int i = 0; i < nh; ++i) {
-                            const uint64_t dX = ssd_desc(aX + i * S::kTile, S::kTile, 1024);
+                        for (int part = kVarParts - 1; part >= 0; --part)
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                ssd_mma_ts(tYd + 64 * i, tG + 16 * k + 8 * i, dX + ((2048 * k) >> 4), id, k > 0);
-                        }
+                                ssd_mma(tS, dB + ((2048 * k) >> 4), dX + ((part * kVarHeads * S::kTile + 2048 * k) >> 4), id, 1);
+                        ssd_commit(mS);
                     }
+                    __syncwarp();
+                    state = true;
+                    nS = u + 1;
                 }
-                ssd_commit(mY);  // (also what was issued before a wait gave up)
-                nY = u + 1;
-                if (!decays) break;
-                go = next(u + 1);
-                if (!ssd_wait(mY, ph, error)) break;
-                wY = u + 1;
-                if (go) load();
+                if (!SUMMARY && !yd && test(bE2, ph)) {
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    if (ssd_elect()) {  // Yd = (C B^T with its decays) x, per head
+                        constexpr uint32_t id = ssd_idesc(128, 64, 0, 1);
+                        const uint64_t dX = ssd_desc(aX, S::kTile, 1024);
+#pragma unroll
+                        for (int i = 0; i < kVarHeads; ++i)
+                            if (i < heads) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    ssd_mma_ts(tYd + 64 * i, tG + 16 * k + 8 * i, dX + ((i * S::kTile + 2048 * k) >> 4), id, k > 0);
+                            }
+                        ssd_commit(mY);
+                    }
+                    __syncwarp();
+                    yd = true;
+                    nY = u + 1;
+                }
             }
-            // nothing in flight when the CTA ends
-            if (nL > wL) {
-                ssd_drain(bX, (nL - 1) & 1u, error);
-                ssd_drain(bCB, (nL - 1) & 1u, error);
-            }
-            if (nG > 0) ssd_drain(mG, (nG - 1) & 1u, error);
-            if (nY > wY) ssd_drain(mY, (nY - 1) & 1u, error);
+            if (!(state && yd)) break;
         }
+        // nothing in flight when the CTA ends (a phase that was waited for before is over: the
+        // test of its parity says so at once)
+        if (nG > 0) ssd_drain(mG, (nG - 1) & 1u, error);
+        if (nC > 0) ssd_drain(mC, (nC - 1) & 1u, error);
+        if (nS > 0) ssd_drain(mS, (nS - 1) & 1u, error);
+        if (nY > 0) ssd_drain(mY, (nY - 1) & 1u, error);
         __syncwarp();
-    } else if (warp == kVarEpilogue / 32 + 1) {
+    } else if (warp == 2 * kVarHalf / 32 + 2) {
+        // ---- the loads: C once C S has read the chunk's before, B once its state's products
+        // have, X once its Yd and the epilogue have ---------------------------------------
+        uint32_t nX = 0, nCB = 0;  // issued in full
+        bool half = false;         // C is on its way without B
+        for (uint32_t u = 0;; ++u) {
+            const uint32_t ph = u & 1u, pv = ph ^ 1u;
+            if (!wait(bFull, ph)) break;
+            const int t0 = info[ph].t0, h0 = info[ph].h0, nh = info[ph].nh, g = info[ph].g;
+            const bool stop = info[ph].stop;
+            __syncwarp();
+            if (lane == 0) ssd_arrive(bEmpty);
+            if (stop) break;
+            bool c = SUMMARY, b = false, x = false;
+            for (uint32_t n = 0; !(c && b && x) && !give_up(n); ++n) {
+                if (!SUMMARY && !c && (u == 0 || test(mC, pv))) {
+                    if (ssd_elect()) {
+                        mbar_arrive_expect_tx(bCB, 2 * S::kTile);
+                        tma_load_3d(sm + S::kC, &tm.C, 0, g, t0, bCB);
+                        tma_load_3d(sm + S::kC + S::kTile, &tm.C, 64, g, t0, bCB);
+                    }
+                    __syncwarp();
+                    c = half = true;
+                }
+                if (!b && c && (u == 0 || test(mS, pv))) {
+                    if (ssd_elect()) {
+                        mbar_arrive_expect_tx(bCB, 2 * S::kTile);
+                        tma_load_3d(sm + S::kB, &tm.B, 0, g, t0, bCB);
+                        tma_load_3d(sm + S::kB + S::kTile, &tm.B, 64, g, t0, bCB);
+                    }
+                    __syncwarp();
+                    b = true;
+                    half = false;
+                    ++nCB;
+                }
+                if (!x && (u == 0 || (test(bE1, pv) && (SUMMARY || test(mY, pv))))) {
+                    if (ssd_elect()) {
+                        mbar_arrive_expect_tx(bX, nh * S::kTile);
+                        for (int i = 0; i < nh; ++i) tma_load_3d(sm + S::kX + i * S::kTile, &tm.x, 0, h0 + i, t0, bX);
+                    }
+                    __syncwarp();
+                    x = true;
+                    ++nX;
+                }
+            }
+            if (!(c && b && x)) break;
+        }
+        // nothing in flight when the CTA ends: a C without its B is let land by completing
+        // the barrier's arrivals
+        if (half) {
+            if (lane == 0) ssd_arrive(bCB);
+            ++nCB;
+        }
+        if (nX > 0) ssd_drain(bX, (nX - 1) & 1u, error);
+        if (nCB > 0) ssd_drain(bCB, (nCB - 1) & 1u, error);
+        __syncwarp();
+    } else if (warp == 2 * kVarHalf / 32 + 1) {
         // ---- table warp: items, running sums and factors.  Half a warp per head, eight
         // rows per lane; the next chunk's dt is on its way while this one's are formed. ----
         const uint32_t sequences = SUMMARY ? 0u : static_cast<uint32_t>(p.seq.sequences);
@@ -517,56 +571,89 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             ssd_arrive(bFull);
         }
         __syncwarp();
-    } else {
-        // ---- epilogue warps: a thread has row 32 quad + lane of every [128][..] tile (its
-        // TMEM lane) and 32 of head `head`'s 64 columns ------------------------------------
-        const int quad = warp & 3, head = (warp >> 2) & 1, c0 = 32 * (warp >> 3), row = quad * 32 + lane;
-        const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-        const uint32_t col = lane_off + 64 * head + c0;
-        uint8_t *xraw = sm + S::kX + head * S::kTile, *stile = sm + S::kS + head * S::kTile;
+    } else if (tid < kVarHalf) {
+        // ---- the state's warps: a thread has row 32 quad + lane of every [128][..] tile (its
+        // TMEM lane) and the 64 columns of head `head` --------------------------------------
+        using L2 = Lanes<2>;
+        const int quad = warp & 3, head = warp >> 2, row = quad * 32 + lane;
+        const uint32_t tSh = tS + (static_cast<uint32_t>(quad * 32) << 16) + 64 * head;
+        const uint8_t *xraw = sm + S::kX + head * S::kTile;
+        uint8_t *stile = sm + S::kS + head * S::kTile;
         uint32_t handed = 0;  // states handed on by this CTA so far
-        bool ok = true;
         for (uint32_t u = 0;; ++u) {
             const uint32_t ph = u & 1u;
-            ok = __all_sync(0xffffffffu, ssd_wait(bFull, ph, error));
-            // read again where it is needed: this chunk's is overwritten only after everyone
-            // has come to the next chunk's C B^T
+            if (u > 0) {
+                if (!__all_sync(0xffffffffu, ssd_wait(mS, ph ^ 1u, error))) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                // the state after an item leaves before anything waits for the next chunk, which
+                // may need it; handed on once every thread's part is written
+                const VarChunk &c = info[ph ^ 1u];
+                if (float *dst = c.dst; c.last && dst) {
+                    if (head < c.nh) {
+#pragma unroll
+                        for (int q0 = 0; q0 < 64; q0 += 16) {
+                            float v[16];
+                            ssd_ld16(tSh + q0, v);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) dst[(head * kSsdP + q0 + e) * kSsdN + row] = v[e];
+                        }
+                    }
+                    if (c.flag) {
+                        ssd_arrive(bOut);
+                        if (tid == 0 && ssd_wait(bOut, handed & 1u, error)) {
+                            __threadfence();  // everyone's part, seen through the barrier, before the flag
+                            st_release(c.flag, 1u);
+                        }
+                        ++handed;
+                        __syncwarp();
+                    }
+                }
+            }
+            if (!__all_sync(0xffffffffu, ssd_wait(bFull, ph, error))) break;
             const VarChunk &c = info[ph];
-            if (!ok || c.stop) break;
+            if (c.stop) break;
             const int rows = c.rows;
             const bool first = c.first, live = head < c.nh;
-            const float decay = c.decay[head];
-            const int fac0 = c.factored[0], fac1 = c.factored[1];
-            const float di0 = tabD[row], di1 = tabD[kVarQ + row];
-            const float di = head ? di1 : di0;
+            const float *src = c.src;
+            const L2 decay = lanes<2>(c.decay[head]);
             float w = tabW[head * kVarQ + row];
-            if (!(head ? fac1 : fac0)) w *= expf(-di);
-            if constexpr (SUMMARY) ssd_arrive(bEmpty);
+            if (!c.factored[head]) w *= expf(-tabD[head * kVarQ + row]);
+            ssd_arrive(bEmpty);
 
-            // S as bf16 to its operand tile [n][p]; exp(T) S, float32, to tensor memory
-#pragma unroll
-            for (int q0 = 0; q0 < 32; q0 += 16) {
-                float v[16];
-                if (!first) {
-                    ssd_ld16(tS + col + q0, v);
-                } else if (const float *src = c.src; src && live) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = __ldcg(src + (head * kSsdP + c0 + q0 + e) * kSsdN + row);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = 0.0f;
-                }
+            // S as bf16 to its operand tile [n][p] (the y before passed through it); exp(T) S,
+            // float32, to tensor memory
+            if (!SUMMARY && u > 0 && !__all_sync(0xffffffffu, ssd_wait(bYf, ph ^ 1u, error))) break;
+            auto put = [&](int q0, const float (&v)[16]) {
                 uint32_t r[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(decay * v[e]);
-                ssd_st16(tS + col + q0, r);
+                for (int e = 0; e < 16; e += 2) {
+                    const L2 d = decay * L2::of(v[e], v[e + 1]);
+                    r[e] = __float_as_uint(d.get(0)), r[e + 1] = __float_as_uint(d.get(1));
+                }
+                ssd_st16(tSh + q0, r);
                 if constexpr (!SUMMARY) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        *reinterpret_cast<uint4 *>(stile + ssd_sw128(row, c0 + q0 + 8 * k)) =
+                        *reinterpret_cast<uint4 *>(stile + ssd_sw128(row, q0 + 8 * k)) =
                             make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
                                        pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
                 }
+            };
+#pragma unroll
+            for (int q0 = 0; q0 < 64; q0 += 32) {
+                float v[16], v2[16];
+                if (!first) {
+                    ssd_ld16x2(tSh + q0, v, tSh + q0 + 16, v2);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float *at = src + (head * kSsdP + q0 + e) * kSsdN + row;
+                        v[e] = src && live ? __ldcg(at) : 0.0f;
+                        v2[e] = src && live ? __ldcg(at + 16 * kSsdN) : 0.0f;
+                    }
+                }
+                put(q0, v);
+                put(q0 + 16, v2);
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             if constexpr (!SUMMARY) {
@@ -577,29 +664,24 @@ __global__ void __launch_bounds__(kVarThreads, 1)
 
             // exp(-d) dt x as three bf16 parts; rows past the chunk's end are zeros whatever
             // they hold (another sequence's values, or none)
-            ok = __all_sync(0xffffffffu, ssd_wait(bX, ph, error));
-            if (!ok) break;
+            if (!__all_sync(0xffffffffu, ssd_wait(bX, ph, error))) break;
             const bool in = row < rows && live;
-            uint32_t xr[16];  // the raw row, kept for D x
+            const L2 w2 = lanes<2>(w), minus = lanes<2>(-1.0f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t o = ssd_sw128(row, c0 + 8 * k);
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t o = ssd_sw128(row, 8 * k);
                 uint4 xv = *reinterpret_cast<const uint4 *>(xraw + o);
-                if (!in) {
-                    xv = make_uint4(0, 0, 0, 0);
-                    if (!SUMMARY && live) *reinterpret_cast<uint4 *>(xraw + o) = xv;  // Yd's operand too
-                }
-                xr[4 * k] = xv.x, xr[4 * k + 1] = xv.y, xr[4 * k + 2] = xv.z, xr[4 * k + 3] = xv.w;
+                if (!in) xv = make_uint4(0, 0, 0, 0);
+                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
                 uint32_t part[kVarParts][4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float v0 = w * __uint_as_float(xr[4 * k + e] << 16);
-                    float v1 = w * __uint_as_float(xr[4 * k + e] & 0xffff0000u);
+                    L2 v = w2 * L2::of(__uint_as_float(xw[e] << 16), __uint_as_float(xw[e] & 0xffff0000u));
 #pragma unroll
                     for (int i = 0; i < kVarParts; ++i) {
-                        part[i][e] = pack_bf16x2(v0, v1);
-                        v0 -= __uint_as_float(part[i][e] << 16);
-                        v1 -= __uint_as_float(part[i][e] & 0xffff0000u);
+                        part[i][e] = pack_bf16x2(v.get(0), v.get(1));
+                        if (i + 1 < kVarParts)
+                            v = L2::fma(minus, L2::of(__uint_as_float(part[i][e] << 16), __uint_as_float(part[i][e] & 0xffff0000u)), v);
                     }
                 }
 #pragma unroll
@@ -609,44 +691,77 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             }
             // B's rows past the end meet zeros, but a NaN there would not vanish
             if (rows < kVarQ) {
-                ok = __all_sync(0xffffffffu, ssd_wait(bCB, ph, error));
-                if (!ok) break;
+                if (!__all_sync(0xffffffffu, ssd_wait(bCB, ph, error))) break;
                 if (row >= rows) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        *reinterpret_cast<uint4 *>(sm + S::kB + head * S::kTile + ssd_sw128(row, c0 + 8 * k)) = make_uint4(0, 0, 0, 0);
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4 *>(sm + S::kB + head * S::kTile + ssd_sw128(row, 8 * k)) = make_uint4(0, 0, 0, 0);
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             ssd_arrive(bE1);
-
-            if constexpr (!SUMMARY) {
-                // C B^T with the decays of both heads, as bf16, over its own columns: this
-                // thread's 32 columns j of its row i, 16 at a time
-                ok = __all_sync(0xffffffffu, ssd_wait(mG, ph, error));
-                if (!ok) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        }
+    } else if constexpr (!SUMMARY) {
+        // ---- the output's warps: a thread has row 32 quad + lane and, of C B^T, 64 columns
+        // j, of y, the 64 columns of head `half` ----------------------------------------------
+        using L2 = Lanes<2>;
+        const int quad = warp & 3, half = (warp >> 2) & 1, row = quad * 32 + lane;
+        const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+        uint8_t *xraw = sm + S::kX + half * S::kTile;
+        for (uint32_t u = 0;; ++u) {
+            const uint32_t ph = u & 1u;
+            if (!__all_sync(0xffffffffu, ssd_wait(bFull, ph, error))) break;
+            // read again where it is needed: this chunk's is overwritten only after everyone
+            // has come to the next chunk's C B^T
+            const VarChunk &c = info[ph];
+            if (c.stop) break;
+            const int rows = c.rows;
+            const bool live = half < c.nh;
+            const int fac0 = c.factored[0], fac1 = c.factored[1];
+            const float di0 = tabD[row], di1 = tabD[kVarQ + row];
+            // the raw row, for D x; rows past the end as zeros, also in Yd's operand
+            if (!__all_sync(0xffffffffu, ssd_wait(bX, ph, error))) break;
+            uint32_t xr[32];
 #pragma unroll
-                for (int q0 = 0; q0 < 32; q0 += 16) {
-                    const int j0 = 64 * head + c0 + q0;
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t o = ssd_sw128(row, 8 * k);
+                if (live && row >= rows) *reinterpret_cast<uint4 *>(xraw + o) = make_uint4(0, 0, 0, 0);
+                const uint4 xv = *reinterpret_cast<const uint4 *>(xraw + o);
+                xr[4 * k] = xv.x, xr[4 * k + 1] = xv.y, xr[4 * k + 2] = xv.z, xr[4 * k + 3] = xv.w;
+            }
+            if (rows < kVarQ) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+
+            // C B^T with the decays of both heads, as bf16, over its own columns: this thread's
+            // 64 columns j of its row i, 16 at a time
+            if (!__all_sync(0xffffffffu, ssd_wait(mG, ph, error))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+            for (int q0 = 0; q0 < 64; q0 += 16) {
+                const int j0 = 64 * half + q0;
+                uint32_t r[16];
+                if (j0 > quad * 32 + 31) {  // above the diagonal for every row of the warp
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r[e] = 0;
+                } else {
                     float v[16];
                     ssd_ld16(tG + lane_off + j0, v);
 #pragma unroll
                     for (int e = 0; e < 16; ++e)  // the causal mask, by selection: a zero whatever the later rows hold
                         if (j0 + e > row) v[e] = 0.0f;
-                    uint32_t r[16];
 #pragma unroll
                     for (int i = 0; i < kVarHeads; ++i) {
                         const float4 *wj = reinterpret_cast<const float4 *>(tabW + i * kVarQ + j0);
                         const float dr = i ? di1 : di0;
                         if (i ? fac1 : fac0) {
-                            const float e = expf(dr);
+                            const L2 e = lanes<2>(expf(dr));
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const float4 f = wj[k];
-                                r[8 * i + 2 * k] = pack_bf16x2(v[4 * k] * (e * f.x), v[4 * k + 1] * (e * f.y));
-                                r[8 * i + 2 * k + 1] = pack_bf16x2(v[4 * k + 2] * (e * f.z), v[4 * k + 3] * (e * f.w));
+                                const L2 a = L2::of(v[4 * k], v[4 * k + 1]) * (e * L2::of(f.x, f.y));
+                                const L2 b = L2::of(v[4 * k + 2], v[4 * k + 3]) * (e * L2::of(f.z, f.w));
+                                r[8 * i + 2 * k] = pack_bf16x2(a.get(0), a.get(1));
+                                r[8 * i + 2 * k + 1] = pack_bf16x2(b.get(0), b.get(1));
                             }
                         } else {
                             // (the mask's columns may have factors up to infinity: left out too)
@@ -663,71 +778,54 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                             }
                         }
                     }
-                    ssd_st16(tG + lane_off + j0, r);
                 }
-                ssd_arrive(bEmpty);
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                ssd_arrive(bE2);
+                ssd_st16(tG + lane_off + j0, r);
             }
-
-            ok = __all_sync(0xffffffffu, ssd_wait(mY, ph, error));
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            if constexpr (!SUMMARY) {
-                // y = Yd + exp(d + T) Yo + D x, through this warp's part of the S tile (read by
-                // the products that are done) so that each store writes whole sectors
-                const float eo = expf(di + c.total[head]), D = c.D[head];
-#pragma unroll
-                for (int q0 = 0; q0 < 32; q0 += 16) {
-                    float yd[16], yo[16];
-                    ssd_ld16(tYo + col + q0, yo);
-                    ssd_ld16(tYd + col + q0, yd);
-                    uint32_t pk[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t x = xr[q0 / 2 + e];
-                        pk[e] = pack_bf16x2(fmaf(eo, yo[2 * e], fmaf(D, __uint_as_float(x << 16), yd[2 * e])),
-                                            fmaf(eo, yo[2 * e + 1], fmaf(D, __uint_as_float(x & 0xffff0000u), yd[2 * e + 1])));
-                    }
-                    *reinterpret_cast<uint4 *>(stile + ssd_sw128(row, c0 + q0)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                    *reinterpret_cast<uint4 *>(stile + ssd_sw128(row, c0 + q0 + 8)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-                }
-                __syncwarp();
-                if (live) {
-                    uint16_t *yg = static_cast<uint16_t *>(p.y) + static_cast<int64_t>(c.t0) * p.y_stride + (c.h0 + head) * kSsdP;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = quad * 32 + 8 * k + (lane >> 2), cc = c0 + 8 * (lane & 3);
-                        if (r < rows)
-                            *reinterpret_cast<uint4 *>(yg + r * p.y_stride + cc) =
-                                *reinterpret_cast<const uint4 *>(stile + ssd_sw128(r, cc));
-                    }
-                }
-                __syncwarp();  // the tile is S again in the next chunk
-            }
-            // the state after an item, and its hand-off once every thread's part is written
-            if (float *dst = c.dst; c.last && dst) {
-                if (live) {
-#pragma unroll
-                    for (int q0 = 0; q0 < 32; q0 += 16) {
-                        float v[16];
-                        ssd_ld16(tS + col + q0, v);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) dst[(head * kSsdP + c0 + q0 + e) * kSsdN + row] = v[e];
-                    }
-                }
-                if (c.flag) {
-                    ssd_arrive(bOut);
-                    if (tid == 0 && ssd_wait(bOut, handed & 1u, error)) {
-                        __threadfence();  // everyone's part, seen through the barrier, before the flag
-                        st_release(c.flag, 1u);
-                    }
-                    ++handed;
-                    __syncwarp();
-                }
-            }
+            ssd_arrive(bEmpty);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            ssd_arrive(bE2);
+
+            if (!__all_sync(0xffffffffu, ssd_wait(mY, ph, error))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            // y = Yd + exp(d + T) Yo + D x
+            const uint32_t col = lane_off + 64 * half;
+            const L2 eo = lanes<2>(expf((half ? di1 : di0) + c.total[half])), D = lanes<2>(c.D[half]);
+#pragma unroll
+            for (int q0 = 0; q0 < 64; q0 += 16) {
+                float yd[16], yo[16];
+                ssd_ld16x2(tYo + col + q0, yo, tYd + col + q0, yd);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {  // y takes x's place
+                    const uint32_t x = xr[q0 / 2 + e];
+                    const L2 v = L2::fma(eo, L2::of(yo[2 * e], yo[2 * e + 1]),
+                                         L2::fma(D, L2::of(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)),
+                                                 L2::of(yd[2 * e], yd[2 * e + 1])));
+                    xr[q0 / 2 + e] = pack_bf16x2(v.get(0), v.get(1));
+                }
+            }
+            // through this warp's rows of the S tile (its product with C is done, and the next
+            // S is written after bYf), so that each store writes whole 128-byte lines
+            uint8_t *stage = sm + S::kS + half * S::kTile;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4 *>(stage + ssd_sw128(row, 8 * k)) = make_uint4(xr[4 * k], xr[4 * k + 1], xr[4 * k + 2], xr[4 * k + 3]);
+            __syncwarp();
+            uint4 line[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                line[k] = *reinterpret_cast<const uint4 *>(stage + ssd_sw128(quad * 32 + 4 * k + (lane >> 3), 8 * (lane & 7)));
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            ssd_arrive(bYf);
+            if (live) {
+                const int r0 = quad * 32 + (lane >> 3);
+                uint16_t *yg = static_cast<uint16_t *>(p.y) + static_cast<int64_t>(c.t0 + r0) * p.y_stride + (c.h0 + half) * kSsdP + 8 * (lane & 7);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (r0 + 4 * k < rows) *reinterpret_cast<uint4 *>(yg) = line[k];
+                    yg += 4 * p.y_stride;
+                }
+            }
         }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
