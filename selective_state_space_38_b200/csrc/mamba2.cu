@@ -456,32 +456,45 @@ bool var_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t n, uint6
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int64_t var_segment(int64_t tokens) {
-    const int64_t least = (tokens + kVarMaxWindows - 1) / kVarMaxWindows;
-    return std::max<int64_t>(kVarSegment, (least + kVarQ - 1) / kVarQ * kVarQ);
-}
 int64_t var_pairs(const ssm_ssd_packed_dims_t *d) {
     return d->groups * ((d->heads / d->groups + kVarHeads - 1) / kVarHeads);
 }
 
-// Workspace: [0, 256) header, the list, the flags, the decays, then (16-byte aligned) the carried states.
+// Tokens of a segment: about six segments for each of 148 SMs if all tokens are in
+// long sequences, so that the last ones even out, but no fewer than kVarLeast (a
+// segment's state costs about a chunk) nor more than kVarMost; beyond 16 segments for
+// each SM longer ones again, and kVarMaxWindows of them at most, which bounds the
+// states in the workspace.
+int64_t var_segment(const ssm_ssd_packed_dims_t *d) {
+    const double work = static_cast<double>(d->tokens) * static_cast<double>(var_pairs(d)) / 148.0;
+    double s = std::min<double>(std::max<double>(work / 6.0, kVarLeast), kVarMost);
+    s = std::max(s, std::max(work / 16.0, static_cast<double>(d->tokens) / kVarMaxWindows));
+    return static_cast<int64_t>(std::min<double>((s + kVarQ - 1) / kVarQ, 1 << 23)) * kVarQ;
+}
+
+// Workspace: [0, 256) header, the units, the later segments, the flags, the decays, then (256-byte
+// aligned) the states that pass between segments or CTAs.
 size_t var_layout(const ssm_ssd_packed_dims_t *d, uint8_t *base, VarWork *w) {
-    const int64_t windows = (d->tokens + var_segment(d->tokens) - 1) / var_segment(d->tokens);
+    const int64_t windows = (d->tokens + var_segment(d) - 1) / var_segment(d);
     size_t at = 256;
     const size_t list = at;
     at += static_cast<size_t>(windows) * sizeof(int2);
+    const size_t units = at;
+    at += static_cast<size_t>(d->sequences + 1) * 4;
     const size_t flags = at;
-    at += static_cast<size_t>(windows) * var_pairs(d) * 4;
+    at += kVarMaxCtas * 4;
     const size_t decay = at;
-    if (windows > 1) at += static_cast<size_t>(windows) * d->heads * 4;
+    at += static_cast<size_t>(windows) * d->heads * 4;
     const size_t carry = at = (at + 255) / 256 * 256;
-    if (windows > 1) at += static_cast<size_t>(windows) * d->heads * kSsdP * kSsdN * 4;  // no carries within one segment
+    at += std::max<size_t>(static_cast<size_t>(windows > 1 ? windows : 0) * d->heads, kVarMaxCtas * kVarHeads) * kSsdP * kSsdN * 4;
     if (w) {
         w->queue = reinterpret_cast<uint32_t *>(base);
-        w->extras = reinterpret_cast<uint32_t *>(base + 8);
-        w->several = reinterpret_cast<uint32_t *>(base + 12);
         w->error = reinterpret_cast<uint32_t *>(base + 16);
-        w->parallel = reinterpret_cast<uint32_t *>(base + 20);
+        w->extras = reinterpret_cast<uint32_t *>(base + 20);
+        w->several = reinterpret_cast<uint32_t *>(base + 24);
+        w->parallel = reinterpret_cast<uint32_t *>(base + 28);
+        w->range = reinterpret_cast<uint32_t *>(base + 32);
+        w->units = reinterpret_cast<uint32_t *>(base + units);
         w->list = reinterpret_cast<int2 *>(base + list);
         w->flags = reinterpret_cast<uint32_t *>(base + flags);
         w->decay = reinterpret_cast<float *>(base + decay);
@@ -523,12 +536,12 @@ int ssd_varlen_impl(const void *x, const void *dt, const float *dt_bias, int sof
     p.seq.tokens = T, p.seq.sequences = static_cast<int32_t>(dims->sequences), p.seq.nslots = static_cast<int32_t>(dims->slots);
     p.dt_stride = dims->dt_stride, p.y_stride = dims->y_stride;
     p.heads = static_cast<int32_t>(H), p.groups = static_cast<int32_t>(G), p.pairs = static_cast<int32_t>(var_pairs(dims));
-    p.segment = static_cast<int32_t>(var_segment(T));
+    p.segment = static_cast<int32_t>(var_segment(dims));
     p.windows = static_cast<int32_t>((T + p.segment - 1) / p.segment);
     p.flag_want = flag_want, p.spin_limit = spin_limit, p.softplus = softplus ? 1 : 0;
     var_layout(dims, static_cast<uint8_t *>(workspace), &p.work);
-    const int64_t items = (dims->sequences + p.windows) * p.pairs;  // at most
-    if (items > INT32_MAX) return SSM_ERR_UNSUPPORTED;
+    const int64_t units = (T / kVarQ + dims->sequences) * p.pairs;  // chunks of all pairs, at most
+    if (units > INT32_MAX / 16) return SSM_ERR_UNSUPPORTED;
     VarMaps tm;
     memset(&tm, 0, sizeof tm);
     if (!var_map(&tm.x, x, kSsdP, H, T, dims->x_stride) || !var_map(&tm.B, B, kSsdN, G, T, dims->b_stride) ||
@@ -536,12 +549,12 @@ int ssd_varlen_impl(const void *x, const void *dt, const float *dt_bias, int sof
         return SSM_ERR_CUDA;
     int sms = 0;
     if (current_sms(&sms) != SSM_OK) return SSM_ERR_CUDA;
-    p.sms = sms;
+    p.ctas = static_cast<int32_t>(std::min<int64_t>({units, sms, kVarMaxCtas}));
     if (cudaFuncSetAttribute(ssd_varlen_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, VarSmem::kTotal) != cudaSuccess ||
         cudaFuncSetAttribute(ssd_varlen_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, VarSmem::kTotal) != cudaSuccess)
         return SSM_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(items, sms));
+    const unsigned ctas = static_cast<unsigned>(p.ctas);
     ssd_varlen_setup_kernel<<<1, 1024, 0, s>>>(p);
     if (p.windows > 1) {  // some sequence may have more than one segment
         const unsigned several = static_cast<unsigned>(std::min<int64_t>({dims->sequences, p.windows, 64}));
@@ -557,7 +570,8 @@ int ssd_varlen_impl(const void *x, const void *dt, const float *dt_bias, int sof
 extern "C" {
 
 int ssm_ssd_varlen_fwd_workspace_size(const ssm_ssd_packed_dims_t *dims, size_t *bytes) {
-    if (!dims || !bytes || dims->tokens < 1 || dims->heads < 1 || dims->groups < 1 || dims->heads % dims->groups != 0)
+    if (!dims || !bytes || dims->tokens < 1 || dims->sequences < 1 || dims->heads < 1 || dims->groups < 1 ||
+        dims->heads % dims->groups != 0)
         return SSM_ERR_INVALID_ARG;
     *bytes = var_layout(dims, nullptr, nullptr);
     return SSM_OK;

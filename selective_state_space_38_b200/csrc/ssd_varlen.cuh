@@ -4,45 +4,48 @@
 //   H_t = exp(dt_t A) H_{t-1} + dt_t x_t B_t^T,   y_t = H_t C_t + D x_t   per head
 //
 // over chunks of Q = 128 steps.  With d_i = cs_i - cs_last (cs the running sum of
-// dt A in the chunk, T its last value) and S the state before the chunk:
+// dt A in the chunk, T its last value), w_j = exp(-d_j) dt_j and S the state before
+// the chunk:
 //
-//   Yd_i  = sum_{j <= i} (C_i . B_j) exp(d_i - d_j) dt_j x_j,   Yo_i = C_i S
-//   y_i   = Yd_i + exp(d_i + T) Yo_i + D x_i
-//   S_new = exp(T) S + sum_j exp(-d_j) dt_j x_j B_j^T
+//   Y_i   = sum_{j <= i} (C_i . B_j) w_j x_j + C_i (exp(T) S),   y_i = exp(d_i) Y_i + D x_i
+//   S_new = exp(T) S + sum_j w_j x_j B_j^T
 //
 // C B^T is the same for every head of a group: it is formed once for the two heads
-// that a CTA walks together.  Where |d| stays below kVarRange = 80 the decays
-// factor, exp(d_i - d_j) dt_j = exp(d_i) w_j with w_j = exp(-d_j) dt_j, the same
-// w_j that scales x for the state; else they are taken element by element.  (With
-// softplus d runs one way, so the factors' product stays below e^80 even where the
-// mask drops it; without it the limit is half of that.  The
-// row factor is not left to the end, though that would save the per-head matrix:
-// the tensor core aligns a sum's products to the largest, and counts a masked zero
-// as 2^-126 times its x; with x scaled over e^110 the first rows of a chunk came
-// out wrong by their whole value, and shorter chunks made heads of strong decay
-// the longest chain.)  The state accumulates in tensor memory on exp(T) S itself.
+// that a CTA walks together; with its columns scaled by w and the later ones masked
+// it meets x itself, and the row factor exp(d_i) waits for the end.  (Scaling x by w
+// instead would save the per-head matrix, but the tensor core aligns a sum's products
+// to the largest and counts a masked zero as 2^-126 times its x: with x scaled over
+// e^110 the first rows of a chunk came out wrong by their whole value.)  Where |d|
+// passes kVarRange the factors would leave bfloat16's range: there the matrix takes
+// its decays element by element against a row factor exp(cs_i), held to e^-70 at
+// least, and S comes unscaled.  The state accumulates in tensor memory on exp(T) S.
 //
-// Roundings to bf16 are those of the tensor core's operands: C B^T with its decays
+// Roundings to bf16 are those of the tensor core's operands: C B^T with its factors
 // once, S once where it meets C (each at most the half step that y's own rounding
-// is), and exp(-d) dt x as a sum of three bf16 parts, 24 bits, where it meets B.
-// The state itself stays float32.  d is summed from the chunk's end, so the steps
-// that count most for the state have the smallest rounding.
+// is), and w x as a sum of three bf16 parts, 24 bits, where it meets B.  The state
+// itself stays float32.  d is summed from the chunk's end, so the steps that count
+// most for the state have the smallest rounding.
 //
 // Per pair of heads and chunk: 96 KB loaded through TMA and six products of
 // 128 x 128 x 128, 3072 cycles of the tensor pipe at 8192 bf16 flops a cycle;
-// shared memory carries about 670 KB for them and their operands, 5200 cycles at
-// 128 bytes a cycle, which bounds the chunk.  One CTA per SM: one warp issues the
-// TMA loads and one the MMAs, a table warp walks the work list a chunk ahead
-// (running sums and factors), and sixteen epilogue warps work in two halves: eight
-// on the state (S and its operand, the parts of x), eight on the output (C B^T with
-// its decays, y), so that a chunk's y is written while the next one's state and
-// operands are formed.  Every wait is bounded.
+// shared memory carries about 640 KB for them and their operands, 5000 cycles at
+// 128 bytes a cycle.  One CTA per SM.  One warp issues the TMA loads and one the MMAs,
+// one walks the work list, one forms the chunks' running sums and factors, and
+// sixteen epilogue warps work in two halves: eight on the state (S and its operand,
+// the parts of w x), eight on the output (C B^T with its factors, y), so that a
+// chunk's y is written while the next one's state and operands are formed.  Every
+// wait is bounded.
 //
-// Long sequences are cut into segments.  Chained, a segment waits for the state of
-// the one before; where that would leave SMs idle (few heads, long sequences) the
-// setup kernel chooses the two-pass schedule instead: the segments' own states
-// first, from zeros and without outputs, all at once, then the states at their
-// starts (ssd_varlen_combine_kernel), then every segment by itself.
+// The work: the chains of chunks (sequence by sequence, pair of heads by pair) form
+// one list, cut into equal ranges, one for each CTA and none shorter than the longest
+// chain.  A range is then the end of one chain (its tail), whole chains, and the
+// start of another (its head): the CTA walks the head first and hands its state on,
+// the tail last, from the state that the CTA before handed on after its own head, so
+// that the wait normally finds it there.  Where the longest chain would leave SMs
+// idle (few heads, long sequences) the setup kernel chooses two passes instead, over
+// segments of the sequences: the segments' own states first, from zeros and without
+// outputs, all at once, then the states at their starts (ssd_varlen_combine_kernel),
+// then every segment by itself.
 #pragma once
 
 #include <cuda.h>
@@ -53,24 +56,30 @@
 namespace ssm {
 
 constexpr int kVarQ = 128;          // steps of a chunk at most
-constexpr int kVarSegment = 1024;   // tokens of a work item at least (all but a sequence's last)
+constexpr int kVarLeast = 256, kVarMost = 896;  // tokens of a segment of the two passes, see var_segment
 constexpr int kVarMaxWindows = 1024;
-constexpr float kVarRange = 80.0f;
+constexpr int kVarMaxCtas = 160;
+constexpr float kVarRange = 70.0f;
 constexpr int kVarHalf = 256;       // epilogue threads on the state, and on the output
-constexpr int kVarThreads = 2 * kVarHalf + 96;  // + a warp for the MMAs, the loads and the tables each
+constexpr int kVarThreads = 2 * kVarHalf + 128;  // + a warp for the MMAs, the tables, the loads and the work list each
 constexpr int kVarHeads = 2;        // heads walked together
-constexpr int kVarParts = 3;        // bf16 parts of exp(-d) dt x
+constexpr int kVarParts = 3;        // bf16 parts of w x
 
-// Workspace: header (error word at 16, where ssm_scan_fwd_status reads it), the
-// work list's later segments, and for each of them (by the window of `segment`
-// tokens it starts in) a flag per pair, a decay and a state per head.
+// Workspace: header (error word at 16, where ssm_scan_fwd_status reads it); the units
+// (chunks x pairs) before each sequence; for the two passes the later segments of the
+// sequences and, by the window of `segment` tokens each starts in, a decay and a state
+// per head; for the ranges a flag and a pair of states per CTA (the states of both
+// share one place).
 struct VarWork {
-    uint32_t *queue, *error, *extras;  // item counters of the passes (2); error word; later segments
-    uint32_t *several, *parallel;      // sequences of more than one segment; the two-pass schedule
+    uint32_t *queue;                   // item counters of the two passes; order of the CTAs' start
+    uint32_t *error, *extras;          // error word; later segments
+    uint32_t *several, *parallel;      // sequences of more than one segment; whether the two passes run
+    uint32_t *range;                   // units of a CTA's range
+    uint32_t *units;                   // [sequences + 1]
     int2 *list;                        // [windows] (sequence, segment) of the later segments
-    uint32_t *flags;                   // [windows][pairs] the state at the segment's start is written
-    float *decay;                      // [windows][heads] of the segment before it
-    float *carry;                      // [windows][heads][P][N] the state at its start
+    uint32_t *flags;                   // [kVarMaxCtas] a range's head is handed on
+    float *decay;                      // [windows][heads] of the segment before the window's
+    float *carry;                      // [windows][heads][P][N], or [kVarMaxCtas][2][P][N]
 };
 
 struct VarMaps {
@@ -86,79 +95,105 @@ struct VarParams {
     VarWork work;
     int64_t dt_stride, y_stride;
     int32_t heads, groups, pairs;  // pairs: of all groups
-    int32_t segment, windows, sms;
+    int32_t segment, windows, ctas;
     uint32_t flag_want, spin_limit;
     int softplus;
+};
+
+// A stretch of a sequence's tokens for a pair of heads, as the work list's warp hands
+// it on: where its state comes from and goes.
+struct VarItem {
+    int32_t first, stop;     // tokens
+    int32_t h0, nh, g;       // first head, heads (1 or 2), group
+    int32_t valid;
+    const float *src;        // the state before it, or NULL (zeros)
+    float *dst;              // where its state goes, or NULL
+    uint32_t *flag;          // hand-off: set once dst is written, or NULL
+    float *decay;            // the two passes' first: receives exp of its sum of dt A, per head
+    float A[2], bias[2], D[2];
 };
 
 // What the table warp hands on with each chunk.
 struct VarChunk {
     int32_t t0, rows;        // first token, steps
-    int32_t h0, nh, g;       // first head, heads (1 or 2), group
+    int32_t h0, nh, g;
     int32_t first, last;     // of the item
     int32_t stop;
-    const float *src;        // the state before the item, or NULL (zeros)
-    float *dst;              // where its state goes, or NULL
-    uint32_t *flag;          // hand-off: set once dst is written, or NULL
-    float decay[2], total[2], D[2];  // exp(T), T
-    int32_t factored[2];
-};
-
-// A segment of a sequence for a pair of heads, as the table warp sees it (A, bias
-// and D: of the lane's head).
-struct VarItem {
-    bool valid, more;        // more: the sequence goes on behind it
-    int32_t h0, nh, g, seg;
-    int64_t first, stop, window;  // window: of the segment's start
-    float *state;
     const float *src;
-    float A, bias, D;
+    float *dst;
+    uint32_t *flag;
+    float decay[2], scale[2], D[2];  // exp(T); of S where it meets C
+    float ref[2];            // cs - ref is the row factor's exponent where the decays are taken one by one
+    int32_t factored[2];
 };
 
 struct VarSmem {
     static constexpr int kTile = 128 * 128;           // [128 rows][64] bf16, 128-byte swizzle
     static constexpr int kC = 0, kB = 2 * kTile;      // [t][n]: n < 64, n >= 64
-    static constexpr int kX = 4 * kTile;              // [t][p] of each head
-    static constexpr int kXp = 6 * kTile;             // exp(-d) dt x: parts x heads tiles
+    static constexpr int kX = 4 * kTile;              // [t][p] of each head; y passes through it
+    static constexpr int kXp = 6 * kTile;             // w x: parts x heads tiles
     static constexpr int kS = kXp + kVarParts * kVarHeads * kTile;  // S [n][p] of each head
     static constexpr int kTabD = kS + kVarHeads * kTile;            // d [head][128]
-    static constexpr int kTabW = kTabD + kVarHeads * 512;           // w where the decays factor, else dt
-    static constexpr int kInfo = kTabW + kVarHeads * 512;
-    static constexpr int kBar = kInfo + 256;                        // of even and of odd chunks
-    static constexpr int kTotal = kBar + 128;
+    static constexpr int kTabW = kTabD + kVarHeads * 512;           // w where the factors are in range, else dt
+    static constexpr int kInfo = kTabW + kVarHeads * 512;           // of even and of odd chunks
+    static constexpr int kItem = kInfo + 256;
+    static constexpr int kBar = kItem + 128;
+    static constexpr int kTotal = kBar + 192;
 };
-static_assert(sizeof(VarChunk) <= 128, "");
+static_assert(sizeof(VarChunk) <= 128 && sizeof(VarItem) <= 128, "");
 static_assert(VarSmem::kTotal <= 227 * 1024, "shared memory of the packed SSD kernel");
 
-// The work list: one segment per sequence first, then the later segments of the
-// longer ones by their number, so that a segment's predecessor always stands
-// before it.  Two later segments never start in the same window of `segment`
-// tokens (those of one sequence are `segment` apart, those of the next sequence
-// start more than that behind its start), so a window's index names one.  One block.
+// The units before each sequence, the later segments ordered by their number (so that
+// the second segments come first), and the choice of the schedule.  Two later segments
+// never start in the same window of `segment` tokens (those of one sequence are
+// `segment` apart, those of the next sequence start more than that behind its start),
+// so a window's index names one.  One block of 1024 threads.
 __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams p) {
     __shared__ int2 at[kVarMaxWindows];
-    __shared__ uint32_t later, several, filled, bad;
+    __shared__ uint32_t sums[32];
+    __shared__ uint32_t later, several, bad;
     __shared__ int longest;
-    if (threadIdx.x == 0) later = 0, several = 0, filled = 0, bad = 0, longest = 1;
-    for (int k = threadIdx.x; k < p.windows; k += blockDim.x) at[k] = make_int2(-1, 0);
-    for (int k = threadIdx.x; k < p.windows * p.pairs; k += blockDim.x) p.work.flags[k] = 0;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) later = 0, several = 0, bad = 0, longest = 0;
+    for (int k = tid; k < p.windows; k += 1024) at[k] = make_int2(-1, 0);
+    for (int k = tid; k < kVarMaxCtas; k += 1024) p.work.flags[k] = 0;
     __syncthreads();
-    for (int n = threadIdx.x; n < p.seq.sequences; n += blockDim.x) {
-        const int32_t a = p.seq.cu[n], b = p.seq.cu[n + 1];
-        if (a < 0 || b < a || b > p.seq.tokens) {
-            bad = 1;
-            continue;
+    uint32_t before = 0;  // units of the sequences of earlier turns
+    for (int n0 = 0; n0 < p.seq.sequences; n0 += 1024) {
+        const int n = n0 + tid;
+        uint32_t units = 0;
+        if (n < p.seq.sequences) {
+            const int32_t a = p.seq.cu[n], b = p.seq.cu[n + 1];
+            if (a < 0 || b < a || b > p.seq.tokens) {
+                bad = 1;
+            } else {
+                const int segs = (b - a + p.segment - 1) / p.segment, chunks = (b - a + kVarQ - 1) / kVarQ;
+                units = static_cast<uint32_t>(chunks) * p.pairs;
+                if (segs > 1) {
+                    for (int s = 1; s < segs; ++s) at[a / p.segment + s] = make_int2(n, s);  // the window of a + s segment
+                    atomicAdd(&several, 1u);
+                }
+                atomicMax(&longest, chunks);
+            }
         }
-        const int segs = (b - a + p.segment - 1) / p.segment;
-        for (int s = 1; s < segs; ++s) at[a / p.segment + s] = make_int2(n, s);  // the window of a + s segment
-        if (segs > 0) atomicAdd(&filled, 1u);
-        if (segs > 1) {
-            atomicAdd(&several, 1u);
-            atomicMax(&longest, segs);
+        uint32_t run = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += v;
         }
+        if (lane == 31) sums[warp] = run;
+        __syncthreads();
+        uint32_t base = before, all = 0;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp) base += sums[w];
+            all += sums[w];
+        }
+        if (n < p.seq.sequences) p.work.units[n + 1] = base + run;
+        before += all;
+        __syncthreads();
     }
-    __syncthreads();
-    for (int k = threadIdx.x; k < p.windows; k += blockDim.x) {
+    for (int k = tid; k < p.windows; k += 1024) {
         const int2 v = at[k];
         if (v.x < 0) continue;
         int rank = 0;
@@ -168,14 +203,16 @@ __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams 
         atomicAdd(&later, 1u);
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        p.work.queue[0] = p.work.queue[1] = 0;
+    if (tid == 0) {
+        p.work.queue[0] = p.work.queue[1] = p.work.queue[2] = 0;
+        p.work.units[0] = 0;
         *p.work.extras = later;
         *p.work.several = several;
-        // the chain of the longest sequence against the segments that each SM takes, with
-        // half as much again for the first pass and two segments for its launches
-        const int64_t items = static_cast<int64_t>(filled + later) * p.pairs;
-        *p.work.parallel = p.flag_want == 1u && 2ll * longest * p.sms > 3ll * items + 4ll * p.sms;
+        // the longest chain against the chunks that each CTA takes: the two passes cost about
+        // 1.4 times those, an uneven last segment, and the launches some four chunks' time
+        const uint32_t each = (before + p.ctas - 1) / p.ctas;
+        *p.work.range = max(max(each, static_cast<uint32_t>(longest)), 1u);
+        *p.work.parallel = p.flag_want == 1u && later > 0 && 10u * longest > 14u * each + 10u * (p.segment / kVarQ + 4);
         *p.work.error = bad ? 4u : 0u;  // a table that does not ascend within the tokens: nothing is run
     }
 }
@@ -187,27 +224,63 @@ __global__ void __launch_bounds__(256) ssd_varlen_combine_kernel(const VarParams
     const int h = blockIdx.x / 8;
     const int64_t e = (blockIdx.x % 8) * 256 + threadIdx.x;  // a 16-byte vector of the state
     for (uint32_t i = blockIdx.y; i < *p.work.several; i += gridDim.y) {
-        const int n = p.work.list[i].x;  // the second segments come first in the list
+        const int n = p.work.list[i].x;
         const int64_t begin = p.seq.cu[n], end = p.seq.cu[n + 1];
         const int segs = static_cast<int>((end - begin + p.segment - 1) / p.segment);
         const int slot = p.states ? packed_slot(p.seq, n) : -1;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (slot >= 0 && p.seq.has_initial && p.seq.has_initial[n])
             s = reinterpret_cast<const float4 *>(p.states + (static_cast<int64_t>(slot) * p.heads + h) * (kSsdP * kSsdN))[e];
-#pragma unroll 4
-        for (int k = 1; k < segs; ++k) {
-            const int64_t at = (begin / p.segment + k) * p.heads + h;
-            float4 *c = reinterpret_cast<float4 *>(p.work.carry + at * (kSsdP * kSsdN)) + e;
-            const float a = p.work.decay[at];
-            const float4 v = *c;
-            s.x = fmaf(a, s.x, v.x), s.y = fmaf(a, s.y, v.y), s.z = fmaf(a, s.z, v.z), s.w = fmaf(a, s.w, v.w);
-            *c = s;
+        for (int k0 = 1; k0 < segs; k0 += 8) {  // eight segments' loads at a time
+            float4 v[8];
+            float a[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t w = (begin / p.segment + min(k0 + j, segs - 1)) * p.heads + h;
+                v[j] = reinterpret_cast<const float4 *>(p.work.carry + w * (kSsdP * kSsdN))[e];
+                a[j] = p.work.decay[w];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (k0 + j >= segs) break;
+                s.x = fmaf(a[j], s.x, v[j].x), s.y = fmaf(a[j], s.y, v[j].y), s.z = fmaf(a[j], s.z, v[j].z), s.w = fmaf(a[j], s.w, v[j].w);
+                reinterpret_cast<float4 *>(p.work.carry + ((begin / p.segment + k0 + j) * p.heads + h) * (kSsdP * kSsdN))[e] = s;
+            }
         }
     }
 }
 
-// SUMMARY: the first pass of the two-pass schedule, which forms the segments' own
-// states only; nothing to do when the setup kernel chose the chained schedule.
+// The chunks of a CTA's range, one item after another (one warp together).
+struct VarRange {
+    // a chain and a place in it
+    struct At {
+        int n, pair, chunk, chunks;
+    };
+    const VarParams &p;
+    __device__ explicit VarRange(const VarParams &q) : p(q) {}
+    __device__ At find(uint32_t unit) const {  // unit < units[sequences]
+        int c = 0;
+        for (int i = threadIdx.x & 31; i < p.seq.sequences; i += 32) c += p.work.units[i + 1] <= unit;
+        At a;
+        a.n = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(c)));
+        const uint32_t from = p.work.units[a.n];
+        a.chunks = static_cast<int>((p.work.units[a.n + 1] - from) / p.pairs);
+        a.pair = static_cast<int>((unit - from) / a.chunks);
+        a.chunk = static_cast<int>((unit - from) % a.chunks);
+        return a;
+    }
+    __device__ void next_chain(At &a) const {
+        a.chunk = 0;
+        if (++a.pair < p.pairs) return;
+        a.pair = 0;
+        do ++a.n;
+        while (a.n < p.seq.sequences && p.work.units[a.n + 1] == p.work.units[a.n]);
+        if (a.n < p.seq.sequences) a.chunks = static_cast<int>((p.work.units[a.n + 1] - p.work.units[a.n]) / p.pairs);
+    }
+};
+
+// SUMMARY: the first of the two passes, which forms the segments' own states only;
+// nothing to do when the setup kernel chose the ranges.
 template <bool SUMMARY>
 __global__ void __launch_bounds__(kVarThreads, 1)
     ssd_varlen_kernel(const VarParams p, const __grid_constant__ VarMaps tm) {
@@ -216,14 +289,16 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     uint8_t *sm = var_smem;
     float *tabD = reinterpret_cast<float *>(sm + S::kTabD), *tabW = reinterpret_cast<float *>(sm + S::kTabW);
     VarChunk *info = reinterpret_cast<VarChunk *>(sm + S::kInfo);
+    VarItem *item = reinterpret_cast<VarItem *>(sm + S::kItem);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + S::kBar);
     uint64_t *bFull = bar, *bX = bar + 1;                          // tables and info written; X landed
-    uint64_t *mG = bar + 2, *mC = bar + 3, *mS = bar + 4, *mY = bar + 5;  // C B^T; C S; the state; Yd done
-    uint64_t *bCB = bar + 6;                                       // C and B landed
-    uint64_t *bEmpty = bar + 7;                                    // info read by everyone, tables done with
-    uint64_t *bS = bar + 8, *bE1 = bar + 9, *bOut = bar + 10;      // S; the parts of x; a handed-on state written
-    uint64_t *bE2 = bar + 11, *bYf = bar + 12;                     // C B^T with its decays written; y out of the S tile
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 13);
+    uint64_t *mG = bar + 2, *mC = bar + 3, *mS = bar + 4, *mY = bar + 5;  // C B^T; C S; the state; Y done
+    uint64_t *bItem = bar + 6, *bTaken = bar + 7;                  // an item written; read
+    uint64_t *bCB = bar + 8;                                       // C and B landed
+    uint64_t *bEmpty = bar + 9;                                    // info read by everyone, tables done with
+    uint64_t *bS = bar + 10, *bE1 = bar + 11, *bOut = bar + 12;    // S; the parts of w x; a handed-on state written
+    uint64_t *bE2 = bar + 13, *bYf = bar + 14;                     // C B^T with its factors written; y out of the X tile
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + 15);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t *error = p.work.error;
 
@@ -236,8 +311,8 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     const bool parallel = *reinterpret_cast<volatile uint32_t *>(p.work.parallel) != 0;
     if (SUMMARY && !parallel) return;
     if (tid == 0) {
-        for (int i = 0; i < 13; ++i) {
-            const uint32_t n = i == 7 ? (SUMMARY ? 1 : 2) * kVarHalf + 2 : i > 7 ? kVarHalf : i == 6 && !SUMMARY ? 2 : 1;
+        for (int i = 0; i < 15; ++i) {
+            const uint32_t n = i < 8 ? 1 : i == 8 ? (SUMMARY ? 1 : 2) : i == 9 ? (SUMMARY ? 1 : 2) * kVarHalf + 2 : kVarHalf;
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar + i)), "r"(n));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -251,31 +326,32 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tbase = *reinterpret_cast<volatile uint32_t *>(tslot);
     // TMEM columns: C B^T (128; its two heads' matrices replace it, as bf16 pairs: of
-    // every 16 columns the first 8 for head 0, the others for head 1), Yd, Yo and S (128
-    // each: head h's column p in 64 h + p; lane n holds S[p][n])
-    const uint32_t tG = tbase, tYd = tbase + 128, tYo = tbase + 256, tS = tbase + 384;
+    // every 16 columns the first 8 for head 0, the others for head 1), Y of even and of odd
+    // chunks and S (128 each: head h's column p in 64 h + p; lane n holds S[p][n])
+    const uint32_t tG = tbase, tY = tbase + 128, tS = tbase + 384;
     constexpr int kN = 64 * kVarHeads;
 
-    // The waits of the two issuing warps, which stay converged: a bounded one, and a test.
+    // The waits of the warps that stay converged: a bounded one, and a test.
     auto wait = [&](uint64_t *b, uint32_t ph) -> bool { return __all_sync(0xffffffffu, ssd_wait(b, ph, error)); };
     auto test = [&](uint64_t *b, uint32_t ph) -> bool { return __any_sync(0xffffffffu, ssd_try(smem_u32(b), ph)); };
     auto give_up = [&](uint32_t n) -> bool {  // after n tests in vain
         if (n >= kSsdWaitLimit && lane == 0) atomicOr(error, 2u);
         return n >= kSsdWaitLimit || ((n & 1023u) == 1023u && __any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(error) != 0));
     };
-    if (warp == 2 * kVarHalf / 32) {
+    constexpr int kMmaWarp = 2 * kVarHalf / 32, kTableWarp = kMmaWarp + 1, kLoadWarp = kMmaWarp + 2, kListWarp = kMmaWarp + 3;
+    if (warp == kMmaWarp) {
         // ---- the products, issued by one elected lane -----------------------------------
         const uint32_t aC = smem_u32(sm + S::kC), aB = smem_u32(sm + S::kB), aX = smem_u32(sm + S::kX),
                        aXp = smem_u32(sm + S::kXp), aS = smem_u32(sm + S::kS);
         uint32_t nG = 0, nC = 0, nS = 0, nY = 0;  // issued
         for (uint32_t u = 0;; ++u) {
-            const uint32_t ph = u & 1u;
+            const uint32_t ph = u & 1u, tYu = tY + 128 * ph;
             if (!wait(bFull, ph)) break;
             const int heads = info[ph].nh;
             const bool stop = info[ph].stop;
             __syncwarp();
             if (lane == 0) ssd_arrive(bEmpty);
-            // (Yd before has read what C B^T replaces: mY)
+            // (the products before have read what C B^T replaces: mY)
             if (stop || !wait(bCB, ph) || (!SUMMARY && u > 0 && !wait(mY, ph ^ 1u))) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             if constexpr (!SUMMARY) {
@@ -291,25 +367,43 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 }
                 __syncwarp();
                 nG = u + 1;
-                if (!wait(bS, ph)) break;  // (S is written after the y before was read)
+                if (!wait(bS, ph)) break;  // (and this Y, of two chunks before, was read before that chunk's bYf)
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                if (ssd_elect()) {  // Yo = C S
+                if (ssd_elect()) {  // Y = C S
                     constexpr uint32_t id = ssd_idesc(128, kN, 0, 1);
                     const uint64_t dC = ssd_desc(aC, 16, 1024), dS = ssd_desc(aS, S::kTile, 1024);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        ssd_mma(tYo, dC + (((k / 4) * S::kTile + (k % 4) * 32) >> 4), dS + ((2048 * k) >> 4), id, k > 0);
+                        ssd_mma(tYu, dC + (((k / 4) * S::kTile + (k % 4) * 32) >> 4), dS + ((2048 * k) >> 4), id, k > 0);
                     ssd_commit(mC);
                 }
                 __syncwarp();
                 nC = u + 1;
             }
-            // the state's products and Yd, whichever has its operands first
+            // the state's products and the rest of Y, whichever has its operands first
             bool state = false, yd = SUMMARY;
             for (uint32_t n = 0; !(state && yd) && !give_up(n); ++n) {
+                if (!SUMMARY && !yd && test(bE2, ph)) {
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    if (ssd_elect()) {  // Y += (C B^T with its factors) x, per head
+                        constexpr uint32_t id = ssd_idesc(128, 64, 0, 1);
+                        const uint64_t dX = ssd_desc(aX, S::kTile, 1024);
+#pragma unroll
+                        for (int i = 0; i < kVarHeads; ++i)
+                            if (i < heads) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    ssd_mma_ts(tYu + 64 * i, tG + 16 * k + 8 * i, dX + ((i * S::kTile + 2048 * k) >> 4), id, 1);
+                            }
+                        ssd_commit(mY);
+                    }
+                    __syncwarp();
+                    yd = true;
+                    nY = u + 1;
+                }
                 if (!state && test(bE1, ph)) {
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    if (ssd_elect()) {  // S += B^T (exp(-d) dt x), the smallest part first
+                    if (ssd_elect()) {  // S += B^T (w x), the smallest part first
                         constexpr uint32_t id = ssd_idesc(128, kN, 1, 1);
                         const uint64_t dB = ssd_desc(aB, S::kTile, 1024), dX = ssd_desc(aXp, S::kTile, 1024);
 #pragma unroll
@@ -323,24 +417,6 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                     state = true;
                     nS = u + 1;
                 }
-                if (!SUMMARY && !yd && test(bE2, ph)) {
-                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    if (ssd_elect()) {  // Yd = (C B^T with its decays) x, per head
-                        constexpr uint32_t id = ssd_idesc(128, 64, 0, 1);
-                        const uint64_t dX = ssd_desc(aX, S::kTile, 1024);
-#pragma unroll
-                        for (int i = 0; i < kVarHeads; ++i)
-                            if (i < heads) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    ssd_mma_ts(tYd + 64 * i, tG + 16 * k + 8 * i, dX + ((i * S::kTile + 2048 * k) >> 4), id, k > 0);
-                            }
-                        ssd_commit(mY);
-                    }
-                    __syncwarp();
-                    yd = true;
-                    nY = u + 1;
-                }
             }
             if (!(state && yd)) break;
         }
@@ -351,9 +427,9 @@ __global__ void __launch_bounds__(kVarThreads, 1)
         if (nS > 0) ssd_drain(mS, (nS - 1) & 1u, error);
         if (nY > 0) ssd_drain(mY, (nY - 1) & 1u, error);
         __syncwarp();
-    } else if (warp == 2 * kVarHalf / 32 + 2) {
+    } else if (warp == kLoadWarp) {
         // ---- the loads: C once C S has read the chunk's before, B once its state's products
-        // have, X once its Yd and the epilogue have ---------------------------------------
+        // have, X once the state's warps have and y, which passes through it, is out of it ---
         uint32_t nX = 0, nCB = 0;  // issued in full
         bool half = false;         // C is on its way without B
         for (uint32_t u = 0;; ++u) {
@@ -386,7 +462,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                     half = false;
                     ++nCB;
                 }
-                if (!x && (u == 0 || (test(bE1, pv) && (SUMMARY || test(mY, pv))))) {
+                if (!x && (u == 0 || (test(bE1, pv) && (SUMMARY || test(bYf, pv))))) {
                     if (ssd_elect()) {
                         mbar_arrive_expect_tx(bX, nh * S::kTile);
                         for (int i = 0; i < nh; ++i) tma_load_3d(sm + S::kX + i * S::kTile, &tm.x, 0, h0 + i, t0, bX);
@@ -407,166 +483,241 @@ __global__ void __launch_bounds__(kVarThreads, 1)
         if (nX > 0) ssd_drain(bX, (nX - 1) & 1u, error);
         if (nCB > 0) ssd_drain(bCB, (nCB - 1) & 1u, error);
         __syncwarp();
-    } else if (warp == 2 * kVarHalf / 32 + 1) {
-        // ---- table warp: items, running sums and factors.  Half a warp per head, eight
-        // rows per lane; the next chunk's dt is on its way while this one's are formed. ----
-        const uint32_t sequences = SUMMARY ? 0u : static_cast<uint32_t>(p.seq.sequences);
-        const uint32_t total = (sequences + *reinterpret_cast<volatile uint32_t *>(p.work.extras)) * static_cast<uint32_t>(p.pairs);
+    } else if (warp == kListWarp) {
+        // ---- the work list: one item ahead of the table warp ------------------------------
         const int HG = p.heads / p.groups, pairs_per_group = p.pairs / p.groups;
-        const int hh = lane >> 4, sub = lane & 15;
-        uint32_t u = 0;
-        auto fetch = [&]() -> VarItem {  // the next item of the list that has tokens
-            VarItem it;
-            it.valid = false;
-            for (;;) {
+        uint32_t k = 0;  // items handed on
+        auto hand_on = [&](bool valid, int n, int pair, int64_t first, int64_t stop, const float *src, float *dst, uint32_t *flag,
+                           float *decay) -> bool {
+            if (k > 0 && !wait(bTaken, (k - 1) & 1u)) return false;
+            if (lane == 0) {
+                item->valid = valid;
+                if (valid) {
+                    const int g = pair / pairs_per_group, h0 = g * HG + (pair % pairs_per_group) * kVarHeads;
+                    const int nh = min(kVarHeads, (g + 1) * HG - h0);
+                    item->first = static_cast<int>(first), item->stop = static_cast<int>(stop);
+                    item->h0 = h0, item->nh = nh, item->g = g;
+                    item->src = src, item->dst = dst, item->flag = flag, item->decay = decay;
+#pragma unroll
+                    for (int i = 0; i < kVarHeads; ++i) {
+                        const int h = h0 + (i < nh ? i : 0);
+                        item->A[i] = p.A[h];
+                        item->bias[i] = p.dt_bias ? p.dt_bias[h] : 0.0f;
+                        item->D[i] = p.D ? p.D[h] : 0.0f;
+                    }
+                }
+                ssd_arrive(bItem);
+            }
+            __syncwarp();
+            ++k;
+            return true;
+        };
+        auto head_of = [&](int pair) { return (pair / pairs_per_group) * HG + (pair % pairs_per_group) * kVarHeads; };
+        // a sequence's place in the cache for a pair of heads, and whether it goes on from it
+        auto cache = [&](int n, int pair, const float **initial) -> float * {
+            const int slot = p.states ? packed_slot(p.seq, n) : -1;
+            float *s = slot >= 0 ? p.states + (static_cast<int64_t>(slot) * p.heads + head_of(pair)) * (kSsdP * kSsdN) : nullptr;
+            *initial = s && p.seq.has_initial && p.seq.has_initial[n] ? s : nullptr;
+            return s;
+        };
+        bool ok = true;
+        if (parallel) {
+            const uint32_t sequences = SUMMARY ? 0u : static_cast<uint32_t>(p.seq.sequences);
+            const uint32_t total = (sequences + *reinterpret_cast<volatile uint32_t *>(p.work.extras)) * static_cast<uint32_t>(p.pairs);
+            while (ok) {
                 uint32_t q = 0;
                 if (lane == 0) q = atomicAdd(p.work.queue + (SUMMARY ? 1 : 0), 1u);
                 q = __shfl_sync(0xffffffffu, q, 0);
-                if (q >= total) return it;
+                if (q >= total) break;
                 const uint32_t e = q / static_cast<uint32_t>(p.pairs);
                 const int pair = static_cast<int>(q % static_cast<uint32_t>(p.pairs));
-                int n = static_cast<int>(e);
-                it.seg = 0;
-                if (e >= sequences) {
+                int n = static_cast<int>(e), seg = 0;
+                if (SUMMARY || e >= sequences) {
                     const int2 v = p.work.list[e - sequences];
-                    n = v.x, it.seg = SUMMARY ? v.y - 1 : v.y;  // (a later segment's start needs the one before)
+                    n = v.x, seg = SUMMARY ? v.y - 1 : v.y;  // (a later segment's start needs the one before)
                 }
                 const int64_t begin = packed_at(p.seq, n), end = packed_at(p.seq, n + 1);
-                it.first = begin + static_cast<int64_t>(it.seg) * p.segment;
-                it.stop = min(it.first + p.segment, end);
-                if (it.first >= it.stop) continue;
-                it.valid = true;
-                it.more = it.stop < end;
-                it.g = pair / pairs_per_group;
-                it.h0 = it.g * HG + (pair % pairs_per_group) * kVarHeads;
-                it.nh = min(kVarHeads, (it.g + 1) * HG - it.h0);
-                it.window = begin / p.segment + it.seg;
-                const int slot = p.states ? packed_slot(p.seq, n) : -1;
-                it.state = slot >= 0 ? p.states + (static_cast<int64_t>(slot) * p.heads + it.h0) * (kSsdP * kSsdN) : nullptr;
-                it.src = it.state && p.seq.has_initial && p.seq.has_initial[n] ? it.state : nullptr;
-                if (it.seg > 0) it.src = p.work.carry + (it.window * p.heads + it.h0) * (kSsdP * kSsdN);
-                if (SUMMARY) it.src = nullptr;
-                const int h = it.h0 + (hh < it.nh ? hh : 0);
-                it.A = p.A[h];
-                it.bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
-                it.D = p.D ? p.D[h] : 0.0f;
-                return it;
+                const int64_t first = begin + static_cast<int64_t>(seg) * p.segment, stop = min(first + p.segment, end);
+                if (first >= stop) continue;
+                const int64_t window = begin / p.segment + seg;  // of its start; the next one's is the segment behind it
+                const int h0 = head_of(pair);
+                if constexpr (SUMMARY) {
+                    const int64_t w = (window + 1) * p.heads + h0;
+                    ok = hand_on(true, n, pair, first, stop, nullptr, p.work.carry + w * (kSsdP * kSsdN), nullptr, p.work.decay + w);
+                } else {
+                    const float *src;
+                    float *state = cache(n, pair, &src);
+                    if (seg > 0) src = p.work.carry + (window * p.heads + h0) * (kSsdP * kSsdN);
+                    ok = hand_on(true, n, pair, first, stop, src, stop < end ? nullptr : state, nullptr, nullptr);
+                }
             }
+        } else {
+            uint32_t order = 0;  // with hand-offs a CTA's range is its place in the order of start
+            if (lane == 0) order = atomicAdd(p.work.queue + 2, 1u);
+            order = __shfl_sync(0xffffffffu, order, 0);
+            const uint32_t W = *reinterpret_cast<volatile uint32_t *>(p.work.range), all = p.work.units[p.seq.sequences];
+            const uint64_t s0 = static_cast<uint64_t>(order) * W;
+            if (s0 < all) {
+                const uint32_t e0 = static_cast<uint32_t>(min(s0 + W, static_cast<uint64_t>(all)));
+                const VarRange range(p);
+                const VarRange::At from = range.find(static_cast<uint32_t>(s0)), to = range.find(e0 - 1);
+                // chunks [c0, c1) of a chain: its state from the cache or the CTA before, to the
+                // cache or the next CTA
+                auto part = [&](const VarRange::At &a, int c0, int c1) -> bool {
+                    const int64_t begin = packed_at(p.seq, a.n), end = packed_at(p.seq, a.n + 1);
+                    const float *src;
+                    float *dst = cache(a.n, a.pair, &src);
+                    uint32_t *flag = nullptr;
+                    if (c0 > 0) {  // (order > 0: the first range starts with a chain)
+                        bool got = false;
+                        if (lane == 0) {
+                            for (uint32_t i = 0; i < p.spin_limit; ++i) {
+                                if (ld_acquire(p.work.flags + order - 1) >= p.flag_want) {
+                                    got = true;
+                                    break;
+                                }
+                                if ((i & 255u) == 255u && *reinterpret_cast<volatile uint32_t *>(error) != 0) break;
+                                __nanosleep(64);
+                            }
+                            if (!got) atomicOr(error, 2u);
+                        }
+                        if (!__shfl_sync(0xffffffffu, static_cast<int>(got), 0)) return false;
+                        src = p.work.carry + static_cast<int64_t>(order - 1) * kVarHeads * (kSsdP * kSsdN);
+                    }
+                    if (c1 < a.chunks) {
+                        dst = p.work.carry + static_cast<int64_t>(order) * kVarHeads * (kSsdP * kSsdN);
+                        flag = p.work.flags + order;
+                    }
+                    return hand_on(true, a.n, a.pair, begin + static_cast<int64_t>(c0) * kVarQ,
+                                   min(begin + static_cast<int64_t>(c1) * kVarQ, end), src, dst, flag, nullptr);
+                };
+                if (from.n == to.n && from.pair == to.pair) {
+                    ok = part(from, from.chunk, to.chunk + 1);
+                } else {
+                    const bool head = to.chunk + 1 < to.chunks;  // a chain that the next CTA ends
+                    if (head) ok = part(to, 0, to.chunk + 1);
+                    VarRange::At a = from;
+                    if (a.chunk > 0) range.next_chain(a);
+                    for (; ok; range.next_chain(a)) {
+                        const bool at_end = a.n == to.n && a.pair == to.pair;
+                        if (at_end && head) break;
+                        ok = part(a, 0, a.chunks);
+                        if (at_end) break;
+                    }
+                    if (ok && from.chunk > 0) ok = part(from, from.chunk, from.chunks);
+                }
+            }
+        }
+        hand_on(false, 0, 0, 0, 0, nullptr, nullptr, nullptr, nullptr);  // (after a failure too, for those who can still hear it)
+        __syncwarp();
+    } else if (warp == kTableWarp) {
+        // ---- the tables: running sums and factors.  Half a warp per head, eight rows per
+        // lane; the next chunk's dt is on its way while this one's are formed. --------------
+        const int hh = lane >> 4, sub = lane & 15;
+        uint32_t u = 0, k = 0;  // chunks handed on, items taken
+        // the item at hand, with this half's A, bias and D
+        int first_t = 0, stop_t = 0, h0 = 0, nh = 0, g = 0;
+        const float *src = nullptr;
+        float *dst = nullptr, *decay = nullptr;
+        uint32_t *flag = nullptr;
+        float A = 0.0f, bias = 0.0f, D = 0.0f;
+        auto take = [&]() -> bool {  // the next item; false: none
+            const bool got = wait(bItem, k & 1u);
+            if (!got) return false;
+            const bool valid = item->valid;
+            first_t = item->first, stop_t = item->stop, h0 = item->h0, nh = item->nh, g = item->g;
+            src = item->src, dst = item->dst, flag = item->flag, decay = item->decay;
+            A = item->A[hh], bias = item->bias[hh], D = item->D[hh];
+            __syncwarp();
+            if (lane == 0) ssd_arrive(bTaken);
+            ++k;
+            return valid;
         };
         uint16_t raw[8];
-        auto load_dt = [&](const VarItem &it, int64_t t) {
-            const uint16_t *src = static_cast<const uint16_t *>(p.dt) + it.h0 + hh;
+        auto load_dt = [&](int64_t t) {
+            const uint16_t *from = static_cast<const uint16_t *>(p.dt) + h0 + hh;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int64_t r = t + 8 * sub + k;
-                raw[k] = r < it.stop && hh < it.nh ? __ldg(src + r * p.dt_stride) : static_cast<uint16_t>(0);
+            for (int i = 0; i < 8; ++i) {
+                const int64_t r = t + 8 * sub + i;
+                raw[i] = r < stop_t && hh < nh ? __ldg(from + r * p.dt_stride) : static_cast<uint16_t>(0);
             }
         };
-        auto ready = [&]() -> bool {  // everyone has read the chunk before
-            const bool ok = u == 0 || ssd_wait(bEmpty, (u - 1) & 1u, error);
-            return __all_sync(0xffffffffu, ok);
-        };
-        bool ok = true;
-        VarItem it = fetch();
-        if (it.valid) load_dt(it, it.first);
-        while (ok && it.valid) {
-            VarItem nxt;
-            nxt.valid = false;
-            float item_total = 0.0f;
-            for (int64_t t = it.first; t < it.stop; t += kVarQ) {
-                const int rows = static_cast<int>(min(static_cast<int64_t>(kVarQ), it.stop - t));
-                const bool last_chunk = t + rows >= it.stop;
-                float dt[8], d[8];
+        auto ready = [&]() -> bool { return u == 0 || wait(bEmpty, (u - 1) & 1u); };  // everyone has read the chunk before
+        bool ok = true, more = take();
+        int t = first_t;
+        if (more) load_dt(t);
+        float item_total = 0.0f;
+        while (more) {
+            const int rows = min(kVarQ, stop_t - t);
+            const bool first = t == first_t, last = t + rows >= stop_t, mine = hh < nh;
+            float dt[8], d[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    dt[k] = __uint_as_float(static_cast<uint32_t>(raw[k]) << 16) + it.bias;
-                    if (p.softplus) dt[k] = softplus_accurate(dt[k]);
-                    if (8 * sub + k >= rows || hh >= it.nh) dt[k] = 0.0f;
-                }
-                if (!last_chunk) load_dt(it, t + rows);
-                // d_j = minus the sum of the later rows' dt A
-                float after = 0.0f;
-#pragma unroll
-                for (int k = 7; k >= 0; --k) {
-                    d[k] = after;
-                    after -= dt[k] * it.A;
-                }
-                float sum = after;
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) {
-                    const float v = __shfl_down_sync(0xffffffffu, sum, o, 16);
-                    if (sub + o < 16) sum += v;
-                }
-                const float T = -__shfl_sync(0xffffffffu, sum, 0, 16);
-                float later = __shfl_down_sync(0xffffffffu, sum, 1, 16);
-                if (sub == 15) later = 0.0f;
-                float most = 0.0f, w[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    d[k] += later;
-                    most = fmaxf(most, fabsf(d[k]));
-                    w[k] = expf(-d[k]) * dt[k];
-                }
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                const bool factored = most <= (p.softplus ? kVarRange : 0.5f * kVarRange);
-                item_total += T;
-                if (!SUMMARY && !parallel && t == it.first && it.seg > 0) {  // the segment before, taken earlier by some CTA
-                    bool got = false;
-                    if (lane == 0) {
-                        const uint32_t *flag = p.work.flags + it.window * p.pairs + it.g * pairs_per_group +
-                                               (it.h0 - it.g * HG) / kVarHeads;
-                        for (uint32_t i = 0; i < p.spin_limit; ++i) {
-                            if (ld_acquire(flag) >= p.flag_want) {
-                                got = true;
-                                break;
-                            }
-                            if ((i & 255u) == 255u && *reinterpret_cast<volatile uint32_t *>(error) != 0) break;
-                            __nanosleep(64);
-                        }
-                        if (!got) atomicOr(error, 2u);
-                    }
-                    ok = __shfl_sync(0xffffffffu, static_cast<int>(got), 0) != 0;
-                }
-                if (!ok || !ready()) {
-                    ok = false;
-                    break;
-                }
-                float4 *pd = reinterpret_cast<float4 *>(tabD + hh * kVarQ + 8 * sub), *pw = reinterpret_cast<float4 *>(tabW + hh * kVarQ + 8 * sub);
-                pd[0] = make_float4(d[0], d[1], d[2], d[3]), pd[1] = make_float4(d[4], d[5], d[6], d[7]);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (!factored) w[k] = dt[k];
-                pw[0] = make_float4(w[0], w[1], w[2], w[3]), pw[1] = make_float4(w[4], w[5], w[6], w[7]);
-                VarChunk *out = info + (u & 1u);
-                if (sub == 0) {
-                    out->decay[hh] = expf(T), out->total[hh] = T, out->D[hh] = it.D;
-                    out->factored[hh] = factored;
-                    if (SUMMARY && last_chunk && hh < it.nh) p.work.decay[(it.window + 1) * p.heads + it.h0 + hh] = expf(item_total);
-                }
-                if (lane == 0) {
-                    out->t0 = static_cast<int>(t), out->rows = rows;
-                    out->h0 = it.h0, out->nh = it.nh, out->g = it.g;
-                    out->first = t == it.first, out->last = last_chunk;
-                    out->stop = 0;
-                    out->src = it.src;
-                    const bool hand = SUMMARY || (it.more && !parallel);
-                    out->dst = hand ? p.work.carry + ((it.window + 1) * p.heads + it.h0) * (kSsdP * kSsdN)
-                                     : it.more ? nullptr : it.state;
-                    out->flag = hand && !SUMMARY ? p.work.flags + (it.window + 1) * p.pairs + it.g * pairs_per_group +
-                                                        (it.h0 - it.g * HG) / kVarHeads
-                                                  : nullptr;
-                }
-                __syncwarp();
-                if (lane == 0) ssd_arrive(bFull);
-                ++u;
-                // the next item, and its first dt, while this chunk is worked on
-                if (t == it.first) nxt = fetch();
-                if (last_chunk && nxt.valid) load_dt(nxt, nxt.first);
+            for (int i = 0; i < 8; ++i) {
+                dt[i] = __uint_as_float(static_cast<uint32_t>(raw[i]) << 16) + bias;
+                if (p.softplus) dt[i] = softplus_accurate(dt[i]);
+                if (8 * sub + i >= rows || !mine) dt[i] = 0.0f;
             }
-            it = nxt;
+            if (!last) load_dt(t + rows);
+            // d_j = minus the sum of the later rows' dt A
+            float after = 0.0f;
+#pragma unroll
+            for (int i = 7; i >= 0; --i) {
+                d[i] = after;
+                after -= dt[i] * A;
+            }
+            float sum = after;
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) {
+                const float v = __shfl_down_sync(0xffffffffu, sum, o, 16);
+                if (sub + o < 16) sum += v;
+            }
+            const float T = -__shfl_sync(0xffffffffu, sum, 0, 16);
+            float later = __shfl_down_sync(0xffffffffu, sum, 1, 16);
+            if (sub == 15) later = 0.0f;
+            float most = fabsf(T), w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                d[i] += later;
+                most = fmaxf(most, fabsf(d[i]));
+                w[i] = expf(-d[i]) * dt[i];
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const bool factored = most <= kVarRange;
+            item_total = (first ? 0.0f : item_total) + T;
+            if (!ready()) {
+                ok = false;
+                break;
+            }
+            float4 *pd = reinterpret_cast<float4 *>(tabD + hh * kVarQ + 8 * sub), *pw = reinterpret_cast<float4 *>(tabW + hh * kVarQ + 8 * sub);
+            pd[0] = make_float4(d[0], d[1], d[2], d[3]), pd[1] = make_float4(d[4], d[5], d[6], d[7]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (!factored) w[i] = dt[i];
+            pw[0] = make_float4(w[0], w[1], w[2], w[3]), pw[1] = make_float4(w[4], w[5], w[6], w[7]);
+            VarChunk *out = info + (u & 1u);
+            if (sub == 0) {
+                out->decay[hh] = expf(T), out->scale[hh] = factored ? expf(T) : 1.0f, out->D[hh] = D;
+                out->ref[hh] = T, out->factored[hh] = factored;
+                if (SUMMARY && last && mine) decay[hh] = expf(item_total);
+            }
+            if (lane == 0) {
+                out->t0 = t, out->rows = rows;
+                out->h0 = h0, out->nh = nh, out->g = g;
+                out->first = first, out->last = last, out->stop = 0;
+                out->src = src, out->dst = dst, out->flag = flag;
+            }
+            __syncwarp();
+            if (lane == 0) ssd_arrive(bFull);
+            ++u;
+            t += rows;
+            if (last) {
+                more = take();
+                t = first_t;
+                if (more) load_dt(t);
+            }
         }
-        if (ready() && lane == 0) {
+        if (ok && ready() && lane == 0) {
             info[u & 1u].stop = 1;
             ssd_arrive(bFull);
         }
@@ -583,10 +734,10 @@ __global__ void __launch_bounds__(kVarThreads, 1)
         for (uint32_t u = 0;; ++u) {
             const uint32_t ph = u & 1u;
             if (u > 0) {
-                if (!__all_sync(0xffffffffu, ssd_wait(mS, ph ^ 1u, error))) break;
+                if (!wait(mS, ph ^ 1u)) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                // the state after an item leaves before anything waits for the next chunk, which
-                // may need it; handed on once every thread's part is written
+                // the state after an item leaves before anything waits for the next chunk;
+                // handed on once every thread's part is written
                 const VarChunk &c = info[ph ^ 1u];
                 if (float *dst = c.dst; c.last && dst) {
                     if (head < c.nh) {
@@ -609,34 +760,34 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                     }
                 }
             }
-            if (!__all_sync(0xffffffffu, ssd_wait(bFull, ph, error))) break;
+            if (!wait(bFull, ph)) break;
             const VarChunk &c = info[ph];
             if (c.stop) break;
             const int rows = c.rows;
             const bool first = c.first, live = head < c.nh;
             const float *src = c.src;
             const L2 decay = lanes<2>(c.decay[head]);
+            const float scale = c.scale[head];
             float w = tabW[head * kVarQ + row];
             if (!c.factored[head]) w *= expf(-tabD[head * kVarQ + row]);
             ssd_arrive(bEmpty);
 
-            // S as bf16 to its operand tile [n][p] (the y before passed through it); exp(T) S,
-            // float32, to tensor memory
-            if (!SUMMARY && u > 0 && !__all_sync(0xffffffffu, ssd_wait(bYf, ph ^ 1u, error))) break;
+            // exp(T) S, float32, to tensor memory; S, scaled as it meets C, as bf16 to its
+            // operand tile [n][p]
             auto put = [&](int q0, const float (&v)[16]) {
                 uint32_t r[16];
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
-                    const L2 d = decay * L2::of(v[e], v[e + 1]);
-                    r[e] = __float_as_uint(d.get(0)), r[e + 1] = __float_as_uint(d.get(1));
+                    const L2 dv = decay * L2::of(v[e], v[e + 1]);
+                    r[e] = __float_as_uint(dv.get(0)), r[e + 1] = __float_as_uint(dv.get(1));
                 }
                 ssd_st16(tSh + q0, r);
                 if constexpr (!SUMMARY) {
+                    uint32_t b[8];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        *reinterpret_cast<uint4 *>(stile + ssd_sw128(row, q0 + 8 * k)) =
-                            make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                                       pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+                    for (int e = 0; e < 8; ++e) b[e] = pack_bf16x2(scale * v[2 * e], scale * v[2 * e + 1]);
+                    *reinterpret_cast<uint4 *>(stile + ssd_sw128(row, q0)) = make_uint4(b[0], b[1], b[2], b[3]);
+                    *reinterpret_cast<uint4 *>(stile + ssd_sw128(row, q0 + 8)) = make_uint4(b[4], b[5], b[6], b[7]);
                 }
             };
 #pragma unroll
@@ -662,9 +813,9 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 ssd_arrive(bS);
             }
 
-            // exp(-d) dt x as three bf16 parts; rows past the chunk's end are zeros whatever
-            // they hold (another sequence's values, or none)
-            if (!__all_sync(0xffffffffu, ssd_wait(bX, ph, error))) break;
+            // w x as three bf16 parts; rows past the chunk's end are zeros whatever they hold
+            // (another sequence's values, or none)
+            if (!wait(bX, ph)) break;
             const bool in = row < rows && live;
             const L2 w2 = lanes<2>(w), minus = lanes<2>(-1.0f);
 #pragma unroll
@@ -691,7 +842,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             }
             // B's rows past the end meet zeros, but a NaN there would not vanish
             if (rows < kVarQ) {
-                if (!__all_sync(0xffffffffu, ssd_wait(bCB, ph, error))) break;
+                if (!wait(bCB, ph)) break;
                 if (row >= rows) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -711,17 +862,26 @@ __global__ void __launch_bounds__(kVarThreads, 1)
         uint8_t *xraw = sm + S::kX + half * S::kTile;
         for (uint32_t u = 0;; ++u) {
             const uint32_t ph = u & 1u;
-            if (!__all_sync(0xffffffffu, ssd_wait(bFull, ph, error))) break;
+            if (!wait(bFull, ph)) break;
             // read again where it is needed: this chunk's is overwritten only after everyone
             // has come to the next chunk's C B^T
             const VarChunk &c = info[ph];
             if (c.stop) break;
             const int rows = c.rows;
             const bool live = half < c.nh;
+            // where the decays are taken one by one, the row factor's exponent is cs_i, held to
+            // [-70, 85] (beyond, only the state before the chunk would feel it, by e^-70 of
+            // itself; growth by e^85 overflows); c_i = d_i - exponent is left to the matrix
+            float ex[kVarHeads], ci[kVarHeads];
+#pragma unroll
+            for (int i = 0; i < kVarHeads; ++i) {
+                const float di = tabD[i * kVarQ + row];
+                ex[i] = c.factored[i] ? di : fminf(fmaxf(di + c.ref[i], -kVarRange), 85.0f);
+                ci[i] = di - ex[i];
+            }
             const int fac0 = c.factored[0], fac1 = c.factored[1];
-            const float di0 = tabD[row], di1 = tabD[kVarQ + row];
-            // the raw row, for D x; rows past the end as zeros, also in Yd's operand
-            if (!__all_sync(0xffffffffu, ssd_wait(bX, ph, error))) break;
+            // the raw row, for D x; rows past the end as zeros, also in the operand
+            if (!wait(bX, ph)) break;
             uint32_t xr[32];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -732,9 +892,9 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             }
             if (rows < kVarQ) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 
-            // C B^T with the decays of both heads, as bf16, over its own columns: this thread's
-            // 64 columns j of its row i, 16 at a time
-            if (!__all_sync(0xffffffffu, ssd_wait(mG, ph, error))) break;
+            // C B^T with the factors of both heads, as bf16, over its own columns: this
+            // thread's 64 columns j of its row i, 16 at a time
+            if (!wait(mG, ph)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
             for (int q0 = 0; q0 < 64; q0 += 16) {
@@ -746,20 +906,20 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 } else {
                     float v[16];
                     ssd_ld16(tG + lane_off + j0, v);
+                    if (j0 + 15 > quad * 32) {  // the causal mask, by selection: a zero whatever the later rows hold
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)  // the causal mask, by selection: a zero whatever the later rows hold
-                        if (j0 + e > row) v[e] = 0.0f;
+                        for (int e = 0; e < 16; ++e)
+                            if (j0 + e > row) v[e] = 0.0f;
+                    }
 #pragma unroll
                     for (int i = 0; i < kVarHeads; ++i) {
                         const float4 *wj = reinterpret_cast<const float4 *>(tabW + i * kVarQ + j0);
-                        const float dr = i ? di1 : di0;
                         if (i ? fac1 : fac0) {
-                            const L2 e = lanes<2>(expf(dr));
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const float4 f = wj[k];
-                                const L2 a = L2::of(v[4 * k], v[4 * k + 1]) * (e * L2::of(f.x, f.y));
-                                const L2 b = L2::of(v[4 * k + 2], v[4 * k + 3]) * (e * L2::of(f.z, f.w));
+                                const L2 a = L2::of(v[4 * k], v[4 * k + 1]) * L2::of(f.x, f.y);
+                                const L2 b = L2::of(v[4 * k + 2], v[4 * k + 3]) * L2::of(f.z, f.w);
                                 r[8 * i + 2 * k] = pack_bf16x2(a.get(0), a.get(1));
                                 r[8 * i + 2 * k + 1] = pack_bf16x2(b.get(0), b.get(1));
                             }
@@ -767,7 +927,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                             // (the mask's columns may have factors up to infinity: left out too)
                             const float4 *dj = reinterpret_cast<const float4 *>(tabD + i * kVarQ + j0);
                             auto factor = [&](float dc, float dtc, int j) {
-                                return j <= row ? ex2_approx((dr - dc) * kLog2e) * dtc : 0.0f;
+                                return j <= row ? ex2_approx((ci[i] - dc) * kLog2e) * dtc : 0.0f;
                             };
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -786,35 +946,36 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             ssd_arrive(bE2);
 
-            if (!__all_sync(0xffffffffu, ssd_wait(mY, ph, error))) break;
+            const float e_row = expf(half ? ex[1] : ex[0]);
+            if (!wait(mY, ph)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            // y = Yd + exp(d + T) Yo + D x
-            const uint32_t col = lane_off + 64 * half;
-            const L2 eo = lanes<2>(expf((half ? di1 : di0) + c.total[half])), D = lanes<2>(c.D[half]);
+            // y = exp(.) Y + D x
+            const uint32_t col = tY + 128 * ph + lane_off + 64 * half;
+            const L2 eo = lanes<2>(e_row), D = lanes<2>(c.D[half]);
 #pragma unroll
-            for (int q0 = 0; q0 < 64; q0 += 16) {
-                float yd[16], yo[16];
-                ssd_ld16x2(tYo + col + q0, yo, tYd + col + q0, yd);
+            for (int q0 = 0; q0 < 64; q0 += 32) {
+                float y0[16], y1[16];
+                ssd_ld16x2(col + q0, y0, col + q0 + 16, y1);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {  // y takes x's place
+                for (int e = 0; e < 16; ++e) {  // y takes x's place
                     const uint32_t x = xr[q0 / 2 + e];
-                    const L2 v = L2::fma(eo, L2::of(yo[2 * e], yo[2 * e + 1]),
-                                         L2::fma(D, L2::of(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)),
-                                                 L2::of(yd[2 * e], yd[2 * e + 1])));
+                    const float a = e < 8 ? y0[2 * e] : y1[2 * e - 16], b = e < 8 ? y0[2 * e + 1] : y1[2 * e - 15];
+                    const L2 v = L2::fma(eo, L2::of(a, b), D * L2::of(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)));
                     xr[q0 / 2 + e] = pack_bf16x2(v.get(0), v.get(1));
                 }
             }
-            // through this warp's rows of the S tile (its product with C is done, and the next
-            // S is written after bYf), so that each store writes whole 128-byte lines
-            uint8_t *stage = sm + S::kS + half * S::kTile;
+            // through this warp's rows of the X tile (the products have read it, and the
+            // state's warps had before bE1), so that each store writes whole 128-byte lines
+            if (!wait(bE1, ph)) break;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4 *>(stage + ssd_sw128(row, 8 * k)) = make_uint4(xr[4 * k], xr[4 * k + 1], xr[4 * k + 2], xr[4 * k + 3]);
+                *reinterpret_cast<uint4 *>(xraw + ssd_sw128(row, 8 * k)) = make_uint4(xr[4 * k], xr[4 * k + 1], xr[4 * k + 2], xr[4 * k + 3]);
             __syncwarp();
             uint4 line[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                line[k] = *reinterpret_cast<const uint4 *>(stage + ssd_sw128(quad * 32 + 4 * k + (lane >> 3), 8 * (lane & 7)));
+                line[k] = *reinterpret_cast<const uint4 *>(xraw + ssd_sw128(quad * 32 + 4 * k + (lane >> 3), 8 * (lane & 7)));
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next load into it
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             ssd_arrive(bYf);
             if (live) {

@@ -46,8 +46,7 @@ def _check(inp, lens, pad=0, with_states=True, initial=None, seed=0, what=""):
     e = (y[:T].cpu().double() - ry[:T]).norm() / ry[:T].norm()
     assert e <= 5e-3, f"{what}: 2-norm of the error {e:.2e}"
     if with_states:
-        # a chunk ends early at most once per 80 of decay
-        chunks = max(lens) // 128 + 2 + int(float((ref.softplus(inp["dt"].double() + inp["dt_bias"].double()) * inp["A"].double().abs()).sum(0).max()) / 80)
+        chunks = max(lens) // 128 + 2
         untouched = [s for s in range(n + 2) if s not in [int(v) for v, ln in zip(slots, lens) if ln]]
         assert torch.equal(st.cpu()[untouched], states[untouched]), "cache rows of no sequence"
         used = [int(v) for v, ln in zip(slots, lens) if ln]
@@ -85,6 +84,13 @@ def test_segments_hand_the_state_on(L):
     lens = [3, L, 40]
     inp = ref.ssd_inputs(ref.gen(L), sum(lens), 2, 1)
     _check(inp, lens, initial=[False, True, False], what=f"segments L={L}")
+
+
+@pytest.mark.parametrize("H,lens", [(100, [256, 256, 256]), (61, [300, 1, 0, 129, 512, 40]), (8, [128] * 45)])
+def test_ranges_hand_the_state_on(H, lens):
+    """More chains than SMs: a CTA's range begins and ends inside chains."""
+    inp = ref.ssd_inputs(ref.gen(H), sum(lens), H, 1)
+    _check(inp, lens, initial=[i % 2 == 0 for i in range(len(lens))], what=f"ranges H={H}")
 
 
 @pytest.mark.parametrize("dt_range", [(1e-5, 1e-4), (0.5, 2.0), (5.0, 20.0)])
@@ -203,15 +209,16 @@ def test_handoff_wait_timeout_is_reported(spin_limit):
     call on the workspace is right."""
     import selective_state_space_38_b200 as ssm
     lib = ssm.get_lib()
-    H, T = 2, 1500
+    H, lens = 100, [256, 256, 256]  # 150 chains of two chunks on 148 SMs: ranges of three chunks split every third
+    T = sum(lens)
     inp = ref.ssd_inputs(ref.gen(19), T, H, 1)
     d = _dev(inp)
-    dims = ssm.SsdPackedDims(T, 1, 0, H, 64, 1, 128, H * 64, H, 128, 128, H * 64, ssm.SSM_BF16)
+    dims = ssm.SsdPackedDims(T, len(lens), 0, H, 64, 1, 128, H * 64, H, 128, 128, H * 64, ssm.SSM_BF16)
     n = ctypes.c_size_t(0)
     assert lib.ssm_ssd_varlen_fwd_workspace_size(ctypes.byref(dims), ctypes.byref(n)) == 0
     ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
     out = torch.zeros(T, H, 64, dtype=torch.bfloat16, device="cuda")
-    cu = _cu([T])
+    cu = _cu(lens)
     sp = torch.cuda.current_stream().cuda_stream
     args = [d["x"].data_ptr(), d["dt"].data_ptr(), d["dt_bias"].data_ptr(), 1, d["A"].data_ptr(), d["B"].data_ptr(),
             d["C"].data_ptr(), d["D"].data_ptr(), cu.data_ptr(), None, None, None, out.data_ptr(), ws.data_ptr(), n.value]
@@ -219,7 +226,7 @@ def test_handoff_wait_timeout_is_reported(spin_limit):
     assert lib.ssm_scan_fwd_status(ws.data_ptr(), sp) == 5
     assert lib.ssm_ssd_varlen_fwd(*args, ctypes.byref(dims), sp) == 0
     assert lib.ssm_scan_fwd_status(ws.data_ptr(), sp) == 0
-    assert torch.equal(out, _call(inp, [T]))
+    assert torch.equal(out, _call(inp, lens))
 
 
 def test_equal_calls_give_equal_bits_and_graph_replays():
@@ -241,7 +248,7 @@ def test_equal_calls_give_equal_bits_and_graph_replays():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         call(out=out)
-    for lens2 in ([1500, 20, 700], [20, 1500, 700], [0, 2220, 0]):
+    for lens2 in ([1500, 20, 700], [20, 1500, 700], [0, 2220, 0], [740, 740, 740]):
         cu.copy_(_cu(lens2))
         out.zero_()
         graph.replay()
