@@ -32,9 +32,10 @@
 // 128 bytes a cycle.  One CTA per SM.  One warp issues the TMA loads and one the MMAs,
 // one walks the work list, one forms the chunks' running sums and factors, and
 // sixteen epilogue warps work in two halves: eight on the state (S and its operand,
-// the parts of w x), eight on the output (C B^T with its factors, y), so that a
-// chunk's y is written while the next one's state and operands are formed.  Every
-// wait is bounded.
+// the parts of w x), eight on the output (y), so that a chunk's y is written while the
+// next one's state and operands are formed; C B^T takes its factors from all sixteen,
+// as only the warps of the last rows have whole rows of it to do.  Every wait is
+// bounded.
 //
 // The work: the chains of chunks (sequence by sequence, pair of heads by pair) form
 // one list, cut into equal ranges, one for each CTA and none shorter than the longest
@@ -279,6 +280,75 @@ struct VarRange {
     }
 };
 
+// The exponent of a row's factor.  Where the decays are taken one by one it is cs_i,
+// held to [-70, 85] (beyond, only the state before the chunk would feel it, by e^-70
+// of itself; growth by e^85 overflows), and the rest is left to the matrix.
+__device__ __forceinline__ float var_row_exponent(const VarChunk &c, int i, float di) {
+    return c.factored[i] ? di : fminf(fmaxf(di + c.ref[i], -kVarRange), 85.0f);
+}
+
+// C B^T with the factors of both heads, as bf16, over its own columns: of this warp's
+// 32 rows the blocks of 16 columns j that fall to `worker` of four.  One copy of it,
+// called: the warps' loops are straight code of thousands of instructions, and the
+// instruction cache is what they would wait for.
+__device__ __noinline__ void var_factors(const VarChunk &c, const float *tabD, const float *tabW, uint32_t at, int row, int worker) {
+    using L2 = Lanes<2>;
+    const int top = row & ~31;
+    float ci[kVarHeads] = {};
+#pragma unroll
+    for (int i = 0; i < kVarHeads; ++i)
+        if (!c.factored[i]) {
+            const float di = tabD[i * kVarQ + row];
+            ci[i] = di - var_row_exponent(c, i, di);
+        }
+#pragma unroll 1
+    for (int j0 = 16 * worker; j0 < kVarQ; j0 += 64) {
+        uint32_t r[16];
+        if (j0 > top + 31) {  // above the diagonal for every row of the warp
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = 0;
+        } else {
+            float v[16];
+            ssd_ld16(at + j0, v);
+            if (j0 + 15 > top) {  // the causal mask, by selection: a zero whatever the later rows hold
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (j0 + e > row) v[e] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < kVarHeads; ++i) {
+                const float4 *wj = reinterpret_cast<const float4 *>(tabW + i * kVarQ + j0);
+                if (c.factored[i]) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 f = wj[k];
+                        const L2 lo = L2::of(v[4 * k], v[4 * k + 1]) * L2::of(f.x, f.y);
+                        const L2 hi = L2::of(v[4 * k + 2], v[4 * k + 3]) * L2::of(f.z, f.w);
+                        r[8 * i + 2 * k] = pack_bf16x2(lo.get(0), lo.get(1));
+                        r[8 * i + 2 * k + 1] = pack_bf16x2(hi.get(0), hi.get(1));
+                    }
+                } else {
+                    // (the mask's columns may have factors up to infinity: left out too)
+                    const float4 *dj = reinterpret_cast<const float4 *>(tabD + i * kVarQ + j0);
+                    auto factor = [&](float dc, float dtc, int j) {
+                        return j <= row ? ex2_approx((ci[i] - dc) * kLog2e) * dtc : 0.0f;
+                    };
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 f = wj[k], dd = dj[k];
+                        const int j = j0 + 4 * k;
+                        r[8 * i + 2 * k] = pack_bf16x2(v[4 * k] * factor(dd.x, f.x, j), v[4 * k + 1] * factor(dd.y, f.y, j + 1));
+                        r[8 * i + 2 * k + 1] = pack_bf16x2(v[4 * k + 2] * factor(dd.z, f.z, j + 2), v[4 * k + 3] * factor(dd.w, f.w, j + 3));
+                    }
+                }
+            }
+        }
+        ssd_st16(at + j0, r);
+    }
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+
 // SUMMARY: the first of the two passes, which forms the segments' own states only;
 // nothing to do when the setup kernel chose the ranges.
 template <bool SUMMARY>
@@ -312,7 +382,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     if (SUMMARY && !parallel) return;
     if (tid == 0) {
         for (int i = 0; i < 15; ++i) {
-            const uint32_t n = i < 8 ? 1 : i == 8 ? (SUMMARY ? 1 : 2) : i == 9 ? (SUMMARY ? 1 : 2) * kVarHalf + 2 : kVarHalf;
+            const uint32_t n = i < 8 ? 1 : i == 8 ? (SUMMARY ? 1 : 2) : i == 9 ? (SUMMARY ? 1 : 2) * kVarHalf + 2 : i == 13 ? 2 * kVarHalf : kVarHalf;
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar + i)), "r"(n));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -741,7 +811,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 const VarChunk &c = info[ph ^ 1u];
                 if (float *dst = c.dst; c.last && dst) {
                     if (head < c.nh) {
-#pragma unroll
+#pragma unroll 1
                         for (int q0 = 0; q0 < 64; q0 += 16) {
                             float v[16];
                             ssd_ld16(tSh + q0, v);
@@ -770,7 +840,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             const float scale = c.scale[head];
             float w = tabW[head * kVarQ + row];
             if (!c.factored[head]) w *= expf(-tabD[head * kVarQ + row]);
-            ssd_arrive(bEmpty);
+            if constexpr (SUMMARY) ssd_arrive(bEmpty);
 
             // exp(T) S, float32, to tensor memory; S, scaled as it meets C, as bf16 to its
             // operand tile [n][p]
@@ -790,7 +860,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                     *reinterpret_cast<uint4 *>(stile + ssd_sw128(row, q0 + 8)) = make_uint4(b[4], b[5], b[6], b[7]);
                 }
             };
-#pragma unroll
+#pragma unroll 1
             for (int q0 = 0; q0 < 64; q0 += 32) {
                 float v[16], v2[16];
                 if (!first) {
@@ -811,6 +881,11 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 ssd_arrive(bS);
+                if (!wait(mG, ph)) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                var_factors(c, tabD, tabW, tG + (static_cast<uint32_t>(quad * 32) << 16), row, 2 + head);
+                ssd_arrive(bEmpty);  // the tables' last readers
+                ssd_arrive(bE2);
             }
 
             // w x as three bf16 parts; rows past the chunk's end are zeros whatever they hold
@@ -818,7 +893,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             if (!wait(bX, ph)) break;
             const bool in = row < rows && live;
             const L2 w2 = lanes<2>(w), minus = lanes<2>(-1.0f);
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < 8; ++k) {
                 const uint32_t o = ssd_sw128(row, 8 * k);
                 uint4 xv = *reinterpret_cast<const uint4 *>(xraw + o);
@@ -854,8 +929,8 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             ssd_arrive(bE1);
         }
     } else if constexpr (!SUMMARY) {
-        // ---- the output's warps: a thread has row 32 quad + lane and, of C B^T, 64 columns
-        // j, of y, the 64 columns of head `half` ----------------------------------------------
+        // ---- the output's warps: a thread has row 32 quad + lane and, of y, the 64 columns of
+        // head `half` ---------------------------------------------------------------------------
         using L2 = Lanes<2>;
         const int quad = warp & 3, half = (warp >> 2) & 1, row = quad * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
@@ -869,107 +944,48 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             if (c.stop) break;
             const int rows = c.rows;
             const bool live = half < c.nh;
-            // where the decays are taken one by one, the row factor's exponent is cs_i, held to
-            // [-70, 85] (beyond, only the state before the chunk would feel it, by e^-70 of
-            // itself; growth by e^85 overflows); c_i = d_i - exponent is left to the matrix
-            float ex[kVarHeads], ci[kVarHeads];
+            const float e_row = expf(var_row_exponent(c, half, tabD[half * kVarQ + row]));
+            // rows past the end as zeros: they are the products' operand
+            if (rows < kVarQ) {
+                if (!wait(bX, ph)) break;
+                if (live && row >= rows) {
 #pragma unroll
-            for (int i = 0; i < kVarHeads; ++i) {
-                const float di = tabD[i * kVarQ + row];
-                ex[i] = c.factored[i] ? di : fminf(fmaxf(di + c.ref[i], -kVarRange), 85.0f);
-                ci[i] = di - ex[i];
+                    for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4 *>(xraw + ssd_sw128(row, 8 * k)) = make_uint4(0, 0, 0, 0);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
-            const int fac0 = c.factored[0], fac1 = c.factored[1];
-            // the raw row, for D x; rows past the end as zeros, also in the operand
-            if (!wait(bX, ph)) break;
-            uint32_t xr[32];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t o = ssd_sw128(row, 8 * k);
-                if (live && row >= rows) *reinterpret_cast<uint4 *>(xraw + o) = make_uint4(0, 0, 0, 0);
-                const uint4 xv = *reinterpret_cast<const uint4 *>(xraw + o);
-                xr[4 * k] = xv.x, xr[4 * k + 1] = xv.y, xr[4 * k + 2] = xv.z, xr[4 * k + 3] = xv.w;
-            }
-            if (rows < kVarQ) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-
-            // C B^T with the factors of both heads, as bf16, over its own columns: this
-            // thread's 64 columns j of its row i, 16 at a time
             if (!wait(mG, ph)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-#pragma unroll 1
-            for (int q0 = 0; q0 < 64; q0 += 16) {
-                const int j0 = 64 * half + q0;
-                uint32_t r[16];
-                if (j0 > quad * 32 + 31) {  // above the diagonal for every row of the warp
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) r[e] = 0;
-                } else {
-                    float v[16];
-                    ssd_ld16(tG + lane_off + j0, v);
-                    if (j0 + 15 > quad * 32) {  // the causal mask, by selection: a zero whatever the later rows hold
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (j0 + e > row) v[e] = 0.0f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < kVarHeads; ++i) {
-                        const float4 *wj = reinterpret_cast<const float4 *>(tabW + i * kVarQ + j0);
-                        if (i ? fac1 : fac0) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float4 f = wj[k];
-                                const L2 a = L2::of(v[4 * k], v[4 * k + 1]) * L2::of(f.x, f.y);
-                                const L2 b = L2::of(v[4 * k + 2], v[4 * k + 3]) * L2::of(f.z, f.w);
-                                r[8 * i + 2 * k] = pack_bf16x2(a.get(0), a.get(1));
-                                r[8 * i + 2 * k + 1] = pack_bf16x2(b.get(0), b.get(1));
-                            }
-                        } else {
-                            // (the mask's columns may have factors up to infinity: left out too)
-                            const float4 *dj = reinterpret_cast<const float4 *>(tabD + i * kVarQ + j0);
-                            auto factor = [&](float dc, float dtc, int j) {
-                                return j <= row ? ex2_approx((ci[i] - dc) * kLog2e) * dtc : 0.0f;
-                            };
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float4 f = wj[k], dd = dj[k];
-                                const int j = j0 + 4 * k;
-                                r[8 * i + 2 * k] = pack_bf16x2(v[4 * k] * factor(dd.x, f.x, j), v[4 * k + 1] * factor(dd.y, f.y, j + 1));
-                                r[8 * i + 2 * k + 1] = pack_bf16x2(v[4 * k + 2] * factor(dd.z, f.z, j + 2), v[4 * k + 3] * factor(dd.w, f.w, j + 3));
-                            }
-                        }
-                    }
-                }
-                ssd_st16(tG + lane_off + j0, r);
-            }
-            ssd_arrive(bEmpty);
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            var_factors(c, tabD, tabW, tG + lane_off, row, half);
+            ssd_arrive(bEmpty);  // the tables' last readers
             ssd_arrive(bE2);
 
-            const float e_row = expf(half ? ex[1] : ex[0]);
-            if (!wait(mY, ph)) break;
+            // y = exp(.) Y + D x, in x's place in its tile (the products have read it, and the
+            // state's warps had before bE1)
+            if (!wait(mY, ph) || !wait(bE1, ph)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            // y = exp(.) Y + D x
             const uint32_t col = tY + 128 * ph + lane_off + 64 * half;
             const L2 eo = lanes<2>(e_row), D = lanes<2>(c.D[half]);
+#pragma unroll 1
+            for (int q0 = 0; q0 < 64; q0 += 16) {
+                float y[16];
+                ssd_ld16(col + q0, y);
 #pragma unroll
-            for (int q0 = 0; q0 < 64; q0 += 32) {
-                float y0[16], y1[16];
-                ssd_ld16x2(col + q0, y0, col + q0 + 16, y1);
+                for (int k = 0; k < 2; ++k) {
+                    uint4 *at = reinterpret_cast<uint4 *>(xraw + ssd_sw128(row, q0 + 8 * k));
+                    const uint4 xv = *at;
+                    const uint32_t x[4] = {xv.x, xv.y, xv.z, xv.w};
+                    uint32_t o[4];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {  // y takes x's place
-                    const uint32_t x = xr[q0 / 2 + e];
-                    const float a = e < 8 ? y0[2 * e] : y1[2 * e - 16], b = e < 8 ? y0[2 * e + 1] : y1[2 * e - 15];
-                    const L2 v = L2::fma(eo, L2::of(a, b), D * L2::of(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)));
-                    xr[q0 / 2 + e] = pack_bf16x2(v.get(0), v.get(1));
+                    for (int e = 0; e < 4; ++e) {
+                        const L2 v = L2::fma(eo, L2::of(y[8 * k + 2 * e], y[8 * k + 2 * e + 1]),
+                                             D * L2::of(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u)));
+                        o[e] = pack_bf16x2(v.get(0), v.get(1));
+                    }
+                    *at = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
-            // through this warp's rows of the X tile (the products have read it, and the
-            // state's warps had before bE1), so that each store writes whole 128-byte lines
-            if (!wait(bE1, ph)) break;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4 *>(xraw + ssd_sw128(row, 8 * k)) = make_uint4(xr[4 * k], xr[4 * k + 1], xr[4 * k + 2], xr[4 * k + 3]);
+            // out of it by whole 128-byte lines, this warp's rows
             __syncwarp();
             uint4 line[8];
 #pragma unroll
