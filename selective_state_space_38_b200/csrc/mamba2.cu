@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <initializer_list>
 #include <type_traits>
@@ -460,16 +461,18 @@ int64_t var_pairs(const ssm_ssd_packed_dims_t *d) {
     return d->groups * ((d->heads / d->groups + kVarHeads - 1) / kVarHeads);
 }
 
-// Tokens of a segment: about six segments for each of 148 SMs if all tokens are in
-// long sequences, so that the last ones even out, but no fewer than kVarLeast (a
-// segment's state costs about a chunk) nor more than kVarMost; beyond 16 segments for
-// each SM longer ones again, and kVarMaxWindows of them at most, which bounds the
-// states in the workspace.
+// Tokens of a segment of the two passes: two to seven chunks, about three segments to each of 148
+// SMs (a segment costs about half a chunk more for its state, and the last ones should even out;
+// one sequence of 32768 with 24 heads: 219 us with seven chunks, 250 with four; 20 ragged ones: 85
+// with two, 118 with five); longer where a thousand segments or sixteen to each SM would not do,
+// which bounds the states in the workspace.
 int64_t var_segment(const ssm_ssd_packed_dims_t *d) {
-    const double work = static_cast<double>(d->tokens) * static_cast<double>(var_pairs(d)) / 148.0;
-    double s = std::min<double>(std::max<double>(work / 6.0, kVarLeast), kVarMost);
-    s = std::max(s, std::max(work / 16.0, static_cast<double>(d->tokens) / kVarMaxWindows));
-    return static_cast<int64_t>(std::min<double>((s + kVarQ - 1) / kVarQ, 1 << 23)) * kVarQ;
+    const int64_t chunks = (d->tokens + kVarQ - 1) / kVarQ;
+    const double work = static_cast<double>(chunks) * static_cast<double>(var_pairs(d)) / 148.0;
+    int64_t c = static_cast<int64_t>(std::min(std::max(std::ceil(work / 3.0), 2.0), 7.0));
+    c = std::max<int64_t>(c, static_cast<int64_t>(std::min(work / 16.0, static_cast<double>(chunks))));
+    c = std::max<int64_t>(c, (chunks + kVarMaxWindows - 1) / kVarMaxWindows);
+    return c * kVarQ;
 }
 
 // Workspace: [0, 256) header, the units, the later segments, the flags, the decays, then (256-byte
@@ -492,7 +495,7 @@ size_t var_layout(const ssm_ssd_packed_dims_t *d, uint8_t *base, VarWork *w) {
         w->error = reinterpret_cast<uint32_t *>(base + 16);
         w->extras = reinterpret_cast<uint32_t *>(base + 20);
         w->several = reinterpret_cast<uint32_t *>(base + 24);
-        w->parallel = reinterpret_cast<uint32_t *>(base + 28);
+        w->mode = reinterpret_cast<uint32_t *>(base + 28);
         w->range = reinterpret_cast<uint32_t *>(base + 32);
         w->units = reinterpret_cast<uint32_t *>(base + units);
         w->list = reinterpret_cast<int2 *>(base + list);
@@ -501,6 +504,19 @@ size_t var_layout(const ssm_ssd_packed_dims_t *d, uint8_t *base, VarWork *w) {
         w->carry = reinterpret_cast<float *>(base + carry);
     }
     return at;
+}
+
+// A kernel whose blocks may come while the one before it on the stream still runs; it waits for
+// that one's end itself.
+template <typename... P, typename... A>
+bool launch_after(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaStream_t stream, const A &...args) {
+    cudaLaunchAttribute after;
+    after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    after.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid, cfg.blockDim = block, cfg.dynamicSmemBytes = static_cast<size_t>(smem), cfg.stream = stream;
+    cfg.attrs = &after, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
 int ssd_varlen_impl(const void *x, const void *dt, const float *dt_bias, int softplus, const float *A, const void *B,
@@ -558,10 +574,11 @@ int ssd_varlen_impl(const void *x, const void *dt, const float *dt_bias, int sof
     ssd_varlen_setup_kernel<<<1, 1024, 0, s>>>(p);
     if (p.windows > 1) {  // some sequence may have more than one segment
         const unsigned several = static_cast<unsigned>(std::min<int64_t>({dims->sequences, p.windows, 64}));
-        ssd_varlen_kernel<true><<<ctas, kVarThreads, VarSmem::kTotal, s>>>(p, tm);
-        ssd_varlen_combine_kernel<<<dim3(static_cast<unsigned>(H) * 8, several), 256, 0, s>>>(p);
+        if (!launch_after(ssd_varlen_kernel<true>, dim3(ctas), dim3(kVarThreads), VarSmem::kTotal, s, p, tm) ||
+            !launch_after(ssd_varlen_combine_kernel, dim3(static_cast<unsigned>(H) * 8, several), dim3(256), 0, s, p))
+            return SSM_ERR_CUDA;
     }
-    ssd_varlen_kernel<false><<<ctas, kVarThreads, VarSmem::kTotal, s>>>(p, tm);
+    if (!launch_after(ssd_varlen_kernel<false>, dim3(ctas), dim3(kVarThreads), VarSmem::kTotal, s, p, tm)) return SSM_ERR_CUDA;
     return launched();
 }
 

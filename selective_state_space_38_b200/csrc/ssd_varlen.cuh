@@ -33,20 +33,21 @@
 // one walks the work list, one forms the chunks' running sums and factors, and
 // sixteen epilogue warps work in two halves: eight on the state (S and its operand,
 // the parts of w x), eight on the output (y), so that a chunk's y is written while the
-// next one's state and operands are formed; C B^T takes its factors from all sixteen,
-// as only the warps of the last rows have whole rows of it to do.  Every wait is
-// bounded.
+// next one's state and operands are formed; C B^T takes its factors from all sixteen
+// (only the warps of the last rows have whole rows of it to do): the output's warps
+// have the time for three quarters of them.  Every wait is bounded.
 //
-// The work: the chains of chunks (sequence by sequence, pair of heads by pair) form
-// one list, cut into equal ranges, one for each CTA and none shorter than the longest
-// chain.  A range is then the end of one chain (its tail), whole chains, and the
-// start of another (its head): the CTA walks the head first and hands its state on,
-// the tail last, from the state that the CTA before handed on after its own head, so
-// that the wait normally finds it there.  Where the longest chain would leave SMs
-// idle (few heads, long sequences) the setup kernel chooses two passes instead, over
-// segments of the sequences: the segments' own states first, from zeros and without
-// outputs, all at once, then the states at their starts (ssd_varlen_combine_kernel),
-// then every segment by itself.
+// The work is chains of chunks, one for each sequence and pair of heads.  The setup
+// kernel chooses between three schedules.  Ranges, when no chain is longer than a
+// CTA's share: the chains form one list, cut into equal ranges, one for each CTA.  A
+// range is then the end of one chain (its tail), whole chains, and the start of
+// another (its head): the CTA walks the head first and hands its state on, the tail
+// last, from the state that the CTA before handed on after its own head, so that the
+// wait normally finds it there.  Whole chains, from a queue, the longer sequences'
+// first, when some are longer than that.  And two passes over segments of the
+// sequences when the longest chain would leave the other SMs idle: the segments' own
+// states first, from zeros and without outputs, all at once, then the states at their
+// starts (ssd_varlen_combine_kernel), then every segment by itself.
 #pragma once
 
 #include <cuda.h>
@@ -57,7 +58,6 @@
 namespace ssm {
 
 constexpr int kVarQ = 128;          // steps of a chunk at most
-constexpr int kVarLeast = 256, kVarMost = 896;  // tokens of a segment of the two passes, see var_segment
 constexpr int kVarMaxWindows = 1024;
 constexpr int kVarMaxCtas = 160;
 constexpr float kVarRange = 70.0f;
@@ -74,7 +74,7 @@ constexpr int kVarParts = 3;        // bf16 parts of w x
 struct VarWork {
     uint32_t *queue;                   // item counters of the two passes; order of the CTAs' start
     uint32_t *error, *extras;          // error word; later segments
-    uint32_t *several, *parallel;      // sequences of more than one segment; whether the two passes run
+    uint32_t *several, *mode;          // sequences of more than one segment; the schedule
     uint32_t *range;                   // units of a CTA's range
     uint32_t *units;                   // [sequences + 1]
     int2 *list;                        // [windows] (sequence, segment) of the later segments
@@ -82,6 +82,8 @@ struct VarWork {
     float *decay;                      // [windows][heads] of the segment before the window's
     float *carry;                      // [windows][heads][P][N], or [kVarMaxCtas][2][P][N]
 };
+
+enum VarMode : uint32_t { kVarRanges = 0, kVarTwoPasses = 1, kVarChains = 2 };
 
 struct VarMaps {
     CUtensorMap x, B, C;  // [tokens][heads or groups][64 or 128], boxes of 64 x 1 x 128 rows
@@ -149,13 +151,20 @@ static_assert(VarSmem::kTotal <= 227 * 1024, "shared memory of the packed SSD ke
 // never start in the same window of `segment` tokens (those of one sequence are
 // `segment` apart, those of the next sequence start more than that behind its start),
 // so a window's index names one.  One block of 1024 threads.
+// The kernels of a call follow each other by programmatic dependent launch: each lets
+// the next one's blocks come while it runs, and waits for the one before to be over
+// (its writes seen) before it reads anything of its.
+__device__ __forceinline__ void var_release_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void var_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams p) {
+    var_release_next();
     __shared__ int2 at[kVarMaxWindows];
     __shared__ uint32_t sums[32];
-    __shared__ uint32_t later, several, bad;
+    __shared__ uint32_t later, several, filled, bad;
     __shared__ int longest;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) later = 0, several = 0, bad = 0, longest = 0;
+    if (tid == 0) later = 0, several = 0, filled = 0, bad = 0, longest = 0;
     for (int k = tid; k < p.windows; k += 1024) at[k] = make_int2(-1, 0);
     for (int k = tid; k < kVarMaxCtas; k += 1024) p.work.flags[k] = 0;
     __syncthreads();
@@ -174,6 +183,7 @@ __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams 
                     for (int s = 1; s < segs; ++s) at[a / p.segment + s] = make_int2(n, s);  // the window of a + s segment
                     atomicAdd(&several, 1u);
                 }
+                if (chunks > 0) atomicAdd(&filled, 1u);
                 atomicMax(&longest, chunks);
             }
         }
@@ -209,11 +219,17 @@ __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams 
         p.work.units[0] = 0;
         *p.work.extras = later;
         *p.work.several = several;
-        // the longest chain against the chunks that each CTA takes: the two passes cost about
-        // 1.4 times those, an uneven last segment, and the launches some four chunks' time
-        const uint32_t each = (before + p.ctas - 1) / p.ctas;
-        *p.work.range = max(max(each, static_cast<uint32_t>(longest)), 1u);
-        *p.work.parallel = p.flag_want == 1u && later > 0 && 10u * longest > 14u * each + 10u * (p.segment / kVarQ + 4);
+        // In tenths of a chunk's time: a CTA's share, with six for the start and the end of each
+        // chain; the two passes cost 1.4 times that, an uneven last segment, and their launches
+        // (four chunks' time).  Measured on 24 heads: one sequence of 32768 tokens 219 us in two
+        // passes against some 1300 as chains; 20 sequences, the longest of 2048, 85 against 134.
+        const uint32_t share = (before + p.ctas - 1) / p.ctas;
+        const int64_t each = (10ll * before + 6ll * filled * p.pairs) / p.ctas;
+        const int64_t two = each * 14 / 10 + 10 * (p.segment / kVarQ + 4);
+        *p.work.range = max(share, 1u);
+        *p.work.mode = share >= static_cast<uint32_t>(longest) || p.flag_want != 1u ? kVarRanges
+                       : later > 0 && 10ll * longest > two                          ? kVarTwoPasses
+                                                                                    : kVarChains;
         *p.work.error = bad ? 4u : 0u;  // a table that does not ascend within the tokens: nothing is run
     }
 }
@@ -221,7 +237,9 @@ __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams 
 // The states at the segments' starts from the segments' own: S_{s+1} = exp(T_s) S_s
 // + E_s, in place.  grid: (heads x 8, sequences of more than one segment at most)
 __global__ void __launch_bounds__(256) ssd_varlen_combine_kernel(const VarParams p) {
-    if ((*p.work.error & 4u) || !*p.work.parallel) return;
+    var_release_next();
+    var_wait_previous();
+    if ((*p.work.error & 4u) || *p.work.mode != kVarTwoPasses) return;
     const int h = blockIdx.x / 8;
     const int64_t e = (blockIdx.x % 8) * 256 + threadIdx.x;  // a 16-byte vector of the state
     for (uint32_t i = blockIdx.y; i < *p.work.several; i += gridDim.y) {
@@ -288,65 +306,63 @@ __device__ __forceinline__ float var_row_exponent(const VarChunk &c, int i, floa
 }
 
 // C B^T with the factors of both heads, as bf16, over its own columns: of this warp's
-// 32 rows the blocks of 16 columns j that fall to `worker` of four.  One copy of it,
+// 32 rows the blocks of 16 columns j0, j0 + 32, ... below j1.  One copy of it,
 // called: the warps' loops are straight code of thousands of instructions, and the
 // instruction cache is what they would wait for.
-__device__ __noinline__ void var_factors(const VarChunk &c, const float *tabD, const float *tabW, uint32_t at, int row, int worker) {
+__device__ __noinline__ void var_factors(const VarChunk &c, const float *tabD, const float *tabW, uint32_t at, int row, int j0,
+                                         int j1) {
     using L2 = Lanes<2>;
     const int top = row & ~31;
-    float ci[kVarHeads] = {};
-#pragma unroll
-    for (int i = 0; i < kVarHeads; ++i)
-        if (!c.factored[i]) {
-            const float di = tabD[i * kVarQ + row];
-            ci[i] = di - var_row_exponent(c, i, di);
-        }
 #pragma unroll 1
-    for (int j0 = 16 * worker; j0 < kVarQ; j0 += 64) {
-        uint32_t r[16];
-        if (j0 > top + 31) {  // above the diagonal for every row of the warp
-#pragma unroll
-            for (int e = 0; e < 16; ++e) r[e] = 0;
-        } else {
-            float v[16];
+    for (; j0 < j1; j0 += 32) {
+        const bool some = j0 <= top + 31;  // else above the diagonal for every row of the warp
+        float v[16];
+        if (some) {
             ssd_ld16(at + j0, v);
             if (j0 + 15 > top) {  // the causal mask, by selection: a zero whatever the later rows hold
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     if (j0 + e > row) v[e] = 0.0f;
             }
+        }
 #pragma unroll
-            for (int i = 0; i < kVarHeads; ++i) {
-                const float4 *wj = reinterpret_cast<const float4 *>(tabW + i * kVarQ + j0);
-                if (c.factored[i]) {
+        for (int i = 0; i < kVarHeads; ++i) {
+            uint32_t r[8] = {};
+            const float4 *wj = reinterpret_cast<const float4 *>(tabW + i * kVarQ + j0);
+            if (some && c.factored[i]) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 f = wj[k];
-                        const L2 lo = L2::of(v[4 * k], v[4 * k + 1]) * L2::of(f.x, f.y);
-                        const L2 hi = L2::of(v[4 * k + 2], v[4 * k + 3]) * L2::of(f.z, f.w);
-                        r[8 * i + 2 * k] = pack_bf16x2(lo.get(0), lo.get(1));
-                        r[8 * i + 2 * k + 1] = pack_bf16x2(hi.get(0), hi.get(1));
-                    }
-                } else {
-                    // (the mask's columns may have factors up to infinity: left out too)
-                    const float4 *dj = reinterpret_cast<const float4 *>(tabD + i * kVarQ + j0);
-                    auto factor = [&](float dc, float dtc, int j) {
-                        return j <= row ? ex2_approx((ci[i] - dc) * kLog2e) * dtc : 0.0f;
-                    };
+                for (int k = 0; k < 4; ++k) {
+                    const float4 f = wj[k];
+                    const L2 lo = L2::of(v[4 * k], v[4 * k + 1]) * L2::of(f.x, f.y);
+                    const L2 hi = L2::of(v[4 * k + 2], v[4 * k + 3]) * L2::of(f.z, f.w);
+                    r[2 * k] = pack_bf16x2(lo.get(0), lo.get(1));
+                    r[2 * k + 1] = pack_bf16x2(hi.get(0), hi.get(1));
+                }
+            } else if (some) {
+                // (the mask's columns may have factors up to infinity: left out too)
+                const float4 *dj = reinterpret_cast<const float4 *>(tabD + i * kVarQ + j0);
+                const float di = tabD[i * kVarQ + row], ci = di - var_row_exponent(c, i, di);
+                auto factor = [&](float dc, float dtc, int j) {
+                    return j <= row ? ex2_approx((ci - dc) * kLog2e) * dtc : 0.0f;
+                };
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 f = wj[k], dd = dj[k];
-                        const int j = j0 + 4 * k;
-                        r[8 * i + 2 * k] = pack_bf16x2(v[4 * k] * factor(dd.x, f.x, j), v[4 * k + 1] * factor(dd.y, f.y, j + 1));
-                        r[8 * i + 2 * k + 1] = pack_bf16x2(v[4 * k + 2] * factor(dd.z, f.z, j + 2), v[4 * k + 3] * factor(dd.w, f.w, j + 3));
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const float4 f = wj[k], dd = dj[k];
+                    const int j = j0 + 4 * k;
+                    r[2 * k] = pack_bf16x2(v[4 * k] * factor(dd.x, f.x, j), v[4 * k + 1] * factor(dd.y, f.y, j + 1));
+                    r[2 * k + 1] = pack_bf16x2(v[4 * k + 2] * factor(dd.z, f.z, j + 2), v[4 * k + 3] * factor(dd.w, f.w, j + 3));
                 }
             }
+            ssd_st8(at + j0 + 8 * i, r);
         }
-        ssd_st16(at + j0, r);
     }
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+
+// One copy of the wait, too.
+__device__ __noinline__ bool var_wait(uint64_t *bar, uint32_t parity, uint32_t *error) {
+    return __all_sync(0xffffffffu, ssd_wait(bar, parity, error));
 }
 
 // SUMMARY: the first of the two passes, which forms the segments' own states only;
@@ -356,6 +372,8 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     ssd_varlen_kernel(const VarParams p, const __grid_constant__ VarMaps tm) {
     extern __shared__ __align__(1024) uint8_t var_smem[];
     using S = VarSmem;
+    // without outputs all sixteen epilogue warps work on the state, half the columns each
+    constexpr int kStateThreads = SUMMARY ? 2 * kVarHalf : kVarHalf, kCols = SUMMARY ? 32 : 64;
     uint8_t *sm = var_smem;
     float *tabD = reinterpret_cast<float *>(sm + S::kTabD), *tabW = reinterpret_cast<float *>(sm + S::kTabW);
     VarChunk *info = reinterpret_cast<VarChunk *>(sm + S::kInfo);
@@ -372,17 +390,20 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t *error = p.work.error;
 
+    // (the first pass does not let the next kernels' blocks come while it has work to do:
+    // beside it they cost it 7 %)
+    var_wait_previous();
     // the swizzled tiles need 1024-byte alignment; a work list that was refused has no items
     if ((smem_u32(sm) & 1023u) != 0) {
         if (tid == 0) atomicOr(error, 2u);
         return;
     }
     if (*reinterpret_cast<volatile uint32_t *>(error) & 4u) return;
-    const bool parallel = *reinterpret_cast<volatile uint32_t *>(p.work.parallel) != 0;
-    if (SUMMARY && !parallel) return;
+    const uint32_t mode = *reinterpret_cast<volatile uint32_t *>(p.work.mode);
+    if (SUMMARY && mode != kVarTwoPasses) return;
     if (tid == 0) {
         for (int i = 0; i < 15; ++i) {
-            const uint32_t n = i < 8 ? 1 : i == 8 ? (SUMMARY ? 1 : 2) : i == 9 ? (SUMMARY ? 1 : 2) * kVarHalf + 2 : i == 13 ? 2 * kVarHalf : kVarHalf;
+            const uint32_t n = i < 8 ? 1 : i == 8 ? (SUMMARY ? 1 : 2) : i == 9 ? 2 * kVarHalf + 2 : i == 13 ? 2 * kVarHalf : i < 13 ? kStateThreads : kVarHalf;
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar + i)), "r"(n));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -402,7 +423,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     constexpr int kN = 64 * kVarHeads;
 
     // The waits of the warps that stay converged: a bounded one, and a test.
-    auto wait = [&](uint64_t *b, uint32_t ph) -> bool { return __all_sync(0xffffffffu, ssd_wait(b, ph, error)); };
+    auto wait = [&](uint64_t *b, uint32_t ph) -> bool { return var_wait(b, ph, error); };
     auto test = [&](uint64_t *b, uint32_t ph) -> bool { return __any_sync(0xffffffffu, ssd_try(smem_u32(b), ph)); };
     auto give_up = [&](uint32_t n) -> bool {  // after n tests in vain
         if (n >= kSsdWaitLimit && lane == 0) atomicOr(error, 2u);
@@ -453,7 +474,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             // the state's products and the rest of Y, whichever has its operands first
             bool state = false, yd = SUMMARY;
             for (uint32_t n = 0; !(state && yd) && !give_up(n); ++n) {
-                if (!SUMMARY && !yd && test(bE2, ph)) {
+                if (!SUMMARY && !yd && test(bE2, ph) && test(bX, ph)) {  // (bE2 alone does not say that X has landed)
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     if (ssd_elect()) {  // Y += (C B^T with its factors) x, per head
                         constexpr uint32_t id = ssd_idesc(128, 64, 0, 1);
@@ -591,9 +612,13 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             return s;
         };
         bool ok = true;
-        if (parallel) {
-            const uint32_t sequences = SUMMARY ? 0u : static_cast<uint32_t>(p.seq.sequences);
-            const uint32_t total = (sequences + *reinterpret_cast<volatile uint32_t *>(p.work.extras)) * static_cast<uint32_t>(p.pairs);
+        if (mode != kVarRanges) {
+            // segments: every sequence's first, then the later ones of the list; chains: the
+            // sequences of several segments (whose second ones lead the list), then the others
+            const bool chains = mode == kVarChains;
+            const uint32_t lead = chains ? *reinterpret_cast<volatile uint32_t *>(p.work.several) : SUMMARY ? 0u : static_cast<uint32_t>(p.seq.sequences);
+            const uint32_t rest = chains ? static_cast<uint32_t>(p.seq.sequences) : *reinterpret_cast<volatile uint32_t *>(p.work.extras);
+            const uint32_t total = (lead + rest) * static_cast<uint32_t>(p.pairs);
             while (ok) {
                 uint32_t q = 0;
                 if (lane == 0) q = atomicAdd(p.work.queue + (SUMMARY ? 1 : 0), 1u);
@@ -602,13 +627,15 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 const uint32_t e = q / static_cast<uint32_t>(p.pairs);
                 const int pair = static_cast<int>(q % static_cast<uint32_t>(p.pairs));
                 int n = static_cast<int>(e), seg = 0;
-                if (SUMMARY || e >= sequences) {
-                    const int2 v = p.work.list[e - sequences];
+                if (chains) {
+                    n = e < lead ? p.work.list[e].x : static_cast<int>(e - lead);
+                } else if (SUMMARY || e >= lead) {
+                    const int2 v = p.work.list[e - lead];
                     n = v.x, seg = SUMMARY ? v.y - 1 : v.y;  // (a later segment's start needs the one before)
                 }
                 const int64_t begin = packed_at(p.seq, n), end = packed_at(p.seq, n + 1);
-                const int64_t first = begin + static_cast<int64_t>(seg) * p.segment, stop = min(first + p.segment, end);
-                if (first >= stop) continue;
+                const int64_t first = begin + static_cast<int64_t>(seg) * p.segment, stop = chains ? end : min(first + p.segment, end);
+                if (first >= stop || (chains && e >= lead && end - begin > p.segment)) continue;
                 const int64_t window = begin / p.segment + seg;  // of its start; the next one's is the segment behind it
                 const int h0 = head_of(pair);
                 if constexpr (SUMMARY) {
@@ -792,11 +819,11 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             ssd_arrive(bFull);
         }
         __syncwarp();
-    } else if (tid < kVarHalf) {
+    } else if (tid < kStateThreads) {
         // ---- the state's warps: a thread has row 32 quad + lane of every [128][..] tile (its
-        // TMEM lane) and the 64 columns of head `head` --------------------------------------
+        // TMEM lane) and of head `head`'s columns the kCols from c0 --------------------------
         using L2 = Lanes<2>;
-        const int quad = warp & 3, head = warp >> 2, row = quad * 32 + lane;
+        const int quad = warp & 3, head = (warp >> 2) & 1, row = quad * 32 + lane, c0 = SUMMARY ? 32 * (warp >> 3) : 0;
         const uint32_t tSh = tS + (static_cast<uint32_t>(quad * 32) << 16) + 64 * head;
         const uint8_t *xraw = sm + S::kX + head * S::kTile;
         uint8_t *stile = sm + S::kS + head * S::kTile;
@@ -812,7 +839,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 if (float *dst = c.dst; c.last && dst) {
                     if (head < c.nh) {
 #pragma unroll 1
-                        for (int q0 = 0; q0 < 64; q0 += 16) {
+                        for (int q0 = c0; q0 < c0 + kCols; q0 += 16) {
                             float v[16];
                             ssd_ld16(tSh + q0, v);
 #pragma unroll
@@ -861,7 +888,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 }
             };
 #pragma unroll 1
-            for (int q0 = 0; q0 < 64; q0 += 32) {
+            for (int q0 = c0; q0 < c0 + kCols; q0 += 32) {
                 float v[16], v2[16];
                 if (!first) {
                     ssd_ld16x2(tSh + q0, v, tSh + q0 + 16, v2);
@@ -883,7 +910,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 ssd_arrive(bS);
                 if (!wait(mG, ph)) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                var_factors(c, tabD, tabW, tG + (static_cast<uint32_t>(quad * 32) << 16), row, 2 + head);
+                var_factors(c, tabD, tabW, tG + (static_cast<uint32_t>(quad * 32) << 16), row, 96 + 16 * head, 128);
                 ssd_arrive(bEmpty);  // the tables' last readers
                 ssd_arrive(bE2);
             }
@@ -893,8 +920,8 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             if (!wait(bX, ph)) break;
             const bool in = row < rows && live;
             const L2 w2 = lanes<2>(w), minus = lanes<2>(-1.0f);
-#pragma unroll 2
-            for (int k = 0; k < 8; ++k) {
+#pragma unroll 1
+            for (int k = c0 / 8; k < (c0 + kCols) / 8; ++k) {
                 const uint32_t o = ssd_sw128(row, 8 * k);
                 uint4 xv = *reinterpret_cast<const uint4 *>(xraw + o);
                 if (!in) xv = make_uint4(0, 0, 0, 0);
@@ -920,7 +947,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                 if (!wait(bCB, ph)) break;
                 if (row >= rows) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
+                    for (int k = c0 / 8; k < (c0 + kCols) / 8; ++k)
                         *reinterpret_cast<uint4 *>(sm + S::kB + head * S::kTile + ssd_sw128(row, 8 * k)) = make_uint4(0, 0, 0, 0);
                 }
             }
@@ -956,7 +983,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             }
             if (!wait(mG, ph)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            var_factors(c, tabD, tabW, tG + lane_off, row, half);
+            var_factors(c, tabD, tabW, tG + lane_off, row, 16 * half, 96);
             ssd_arrive(bEmpty);  // the tables' last readers
             ssd_arrive(bE2);
 

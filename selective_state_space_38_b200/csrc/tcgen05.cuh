@@ -95,6 +95,13 @@ __device__ __forceinline__ void ssd_st16(uint32_t taddr, const uint32_t (&r)[16]
         : "memory");
 }
 
+// 8 consecutive 32-bit columns of this thread's TMEM lane from registers
+__device__ __forceinline__ void ssd_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // 4-D tiled TMA load of a box at (c0, c1, c2, c3); completion as bytes on the mbarrier.
 __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int c0, int c1, int c2, int c3,
                                             uint64_t *bar) {

@@ -256,6 +256,21 @@ def test_equal_calls_give_equal_bits_and_graph_replays():
         assert torch.equal(out, call()), lens2
 
 
+@pytest.mark.parametrize("H,lens", [(80, [1024] * 4), (24, [8192]), (24, [50, 1300, 128, 700] * 8)])
+def test_repeated_calls_on_a_full_gpu_give_equal_bits(H, lens):
+    """Every schedule with all SMs busy, eight times: what a missing wait between the warps would show."""
+    import selective_state_space_38_b200 as ssm
+    d = _dev(ref.ssd_inputs(ref.gen(22), sum(lens), H, 1))
+    cu = _cu(lens)
+    states = torch.zeros(len(lens), H, 64, 128, device="cuda")
+    first = None
+    for _ in range(8):
+        y = ssm.ssm_ssd_varlen_fwd(d["x"], d["dt"], d["dt_bias"], True, d["A"], d["B"], d["C"], d["D"], cu, states=states, check=True)
+        if first is None:
+            first = (y, states.clone())
+        assert torch.equal(y, first[0]) and torch.equal(states, first[1])
+
+
 def _step_ref(inp, states, slots):
     x = inp["x"]
     one = dict(inp)

@@ -66,7 +66,7 @@ def test_conv1d_step(m):
 def test_conv1d_bwd(m):
     lib = m.get_lib()
     n = ctypes.c_size_t(0)
-    assert lib.ssm_conv1d_bwd_workspace_size(_conv_dims(m), ctypes.byref(n)) == 0 and n.value == 5 * 128 * 4
+    assert lib.ssm_conv1d_bwd_workspace_size(_conv_dims(m), ctypes.byref(n)) == 0 and n.value == 4 * 5 * 128 * 4  # four tiles of 16 rows
     assert lib.ssm_conv1d_bwd_workspace_size(None, ctypes.byref(n)) == 1
     assert lib.ssm_conv1d_bwd_workspace_size(_conv_dims(m, width=9), ctypes.byref(n)) == 2
 
