@@ -67,19 +67,24 @@ def _rows(t, *, dtype=None, device=None, shape=None, name=""):
         return None, 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if device is not None and t.device != device:
+    size, strides = t.shape, t.stride()
+    if device is not None and t.get_device() != device.index:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    size, strides = t.shape, t.stride()
     if shape is not None and size != shape:
         raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(shape)}")
-    width = 1
-    for i in range(len(size) - 1, 0, -1):
-        n = size[i]
-        if n > 1 and strides[i] != width:
-            raise ValueError(f"{name}: the elements of a row must lie together (strides {strides})")
-        width *= n
+    if len(size) == 2:
+        width = size[1]
+        together = strides[1] == 1 or width == 1
+    elif len(size) == 3:
+        heads, each = size[1], size[2]
+        width = heads * each
+        together = (strides[2] == 1 or each == 1) and (strides[1] == each or heads == 1)
+    else:
+        raise ValueError(f"{name} must have two or three dimensions, got shape {tuple(size)}")
+    if not together:
+        raise ValueError(f"{name}: the elements of a row must lie together (strides {strides})")
     if size[0] <= 1:
         return t.data_ptr(), width
     if strides[0] < width:
@@ -91,7 +96,7 @@ def _flat(t, dtype, device, shape, name):
     """Pointer of a contiguous tensor (None: no tensor); _ptr says what is wrong with others."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
         return t.data_ptr()
     return _ptr(t, dtype=dtype, device=device, shape=shape, name=name)
 
@@ -99,7 +104,7 @@ def _flat(t, dtype, device, shape, name):
 def _cuda(x, rank, name):
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("this operator needs CUDA tensors")
     if x.dim() != rank:
         raise ValueError(f"{name} must have {rank} dimensions, got shape {tuple(x.shape)}")
@@ -116,13 +121,14 @@ class _on:
         self.device, self.stream, self.inside = device, stream, ()
 
     def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
+        index = self.device.index
+        if index != torch._C._cuda_getDevice():
             self.inside += (torch.cuda.device(self.device),)
         if self.stream is not None:
             self.inside += (torch.cuda.stream(self.stream),)
         for c in self.inside:
             c.__enter__()
-        return (self.stream or torch.cuda.current_stream(self.device)).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(index) if self.stream is None else self.stream.cuda_stream
 
     def __exit__(self, *error):
         for c in reversed(self.inside):
