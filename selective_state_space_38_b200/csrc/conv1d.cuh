@@ -147,7 +147,7 @@ struct ConvChannels {
 
 // grid: row tiles x channel blocks, the channel blocks of a tile next to each other
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(kConvThreads) conv1d_fwd_kernel(const Conv1dParams p) {
+__global__ void __launch_bounds__(kConvThreads, 6) conv1d_fwd_kernel(const Conv1dParams p) {
     using R = Row<T, V>;
     constexpr bool kAccurate = Act<T>::kBytes == 4;
     constexpr int kL = R::kL, kN = R::kN;
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kConvThreads) conv1d_step_kernel(const Conv1dP
 // `partial`, which conv1d_reduce_kernel adds in a fixed order: the result does
 // not depend on the order in which blocks run.
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(kConvThreads) conv1d_bwd_kernel(const Conv1dParams p) {
+__global__ void __launch_bounds__(kConvThreads, 4) conv1d_bwd_kernel(const Conv1dParams p) {
     using R = Row<T, V>;
     constexpr bool kAccurate = Act<T>::kBytes == 4;
     constexpr int kL = R::kL, kN = R::kN, kB = kConvBwdBatch;
