@@ -204,7 +204,7 @@ int ssm_conv1d_step(void *windows, const int32_t *slots, const void *x, const fl
 
 int ssm_conv1d_bwd_workspace_size(const ssm_conv1d_dims_t *dims, size_t *bytes) {
     if (!dims || !bytes || dims->tokens < 1 || dims->dim < 1) return SSM_ERR_INVALID_ARG;
-    if (dims->width < 1 || dims->width > 4) return SSM_ERR_UNSUPPORTED;
+    if (dims->width < 1 || dims->width > 4 || dims->tokens > INT32_MAX || dims->dim > INT32_MAX) return SSM_ERR_UNSUPPORTED;
     *bytes = conv_bwd_bytes(dims);
     return SSM_OK;
 }
@@ -374,6 +374,7 @@ int ssm_gated_norm_fwd(const void *x, const void *z, const float *weight, void *
 int ssm_gated_norm_bwd_workspace_size(const ssm_norm_dims_t *dims, size_t *bytes) {
     if (!dims || !bytes || dims->rows < 1 || dims->dim < 1 || dims->groups < 1 || dims->dim % dims->groups != 0)
         return SSM_ERR_INVALID_ARG;
+    if (dims->rows > INT32_MAX || dims->dim > INT32_MAX) return SSM_ERR_UNSUPPORTED;
     *bytes = norm_bwd_bytes(dims);
     return SSM_OK;
 }
@@ -597,6 +598,7 @@ int ssm_ssd_varlen_fwd_workspace_size(const ssm_ssd_packed_dims_t *dims, size_t 
     if (!dims || !bytes || dims->tokens < 1 || dims->sequences < 1 || dims->heads < 1 || dims->groups < 1 ||
         dims->heads % dims->groups != 0)
         return SSM_ERR_INVALID_ARG;
+    if (dims->tokens > INT32_MAX - kVarQ || dims->sequences > INT32_MAX / 4 || dims->heads > 65535) return SSM_ERR_UNSUPPORTED;
     *bytes = var_layout(dims, nullptr, nullptr);
     return SSM_OK;
 }

@@ -61,7 +61,7 @@ EXPORTS = ("ssm_conv1d_fwd", "ssm_conv1d_step", "ssm_conv1d_bwd_workspace_size",
            "ssm_ssd_step", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd_workspace_size", "ssm_gated_norm_bwd")
 
 
-def _rows(t, *, dtype=None, device=None, shape=None, name=""):
+def _rows(t, device=None, name="", dtype=None, shape=None):
     """(pointer, row stride) of a tensor whose rows' elements lie together."""
     if t is None:
         return None, 0
@@ -101,6 +101,11 @@ def _flat(t, dtype, device, shape, name):
     return _ptr(t, dtype=dtype, device=device, shape=shape, name=name)
 
 
+def _like(t):
+    """A new contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _cuda(x, rank, name):
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -118,6 +123,8 @@ class _on:
     __slots__ = ("device", "stream", "inside")
 
     def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         self.device, self.stream, self.inside = device, stream, ()
 
     def __enter__(self):
@@ -170,7 +177,7 @@ def ssm_conv1d_fwd(x, conv_w, conv_bias, cu_seqlens, windows=None, slots=None, h
     act, f32 = x.dtype, torch.float32
     code = _act_code(x)
     K = int(conv_w.shape[1])
-    px, xs = _rows(x, device=dev, name="x")
+    px, xs = _rows(x, dev, "x")
     pw = _flat(conv_w, f32, dev, (dim, K), "conv_w")
     pb = _flat(conv_bias, f32, dev, (dim,), "conv_bias")
     pc, ps, ph, n = _tables(cu_seqlens, slots, has_initial, dev)
@@ -180,8 +187,8 @@ def ssm_conv1d_fwd(x, conv_w, conv_bias, cu_seqlens, windows=None, slots=None, h
     pwin = _flat(windows, act, dev, (nslots, K - 1, dim), "windows")
     with _on(dev, stream) as sp:
         if out is None:
-            out = torch.empty((T, dim), dtype=act, device=dev)
-        po, os_ = _rows(out, dtype=act, device=dev, shape=(T, dim), name="out")
+            out = _like(x)
+        po, os_ = _rows(out, dev, "out", act, (T, dim))
         dims = Conv1dDims(T, dim, n, nslots, xs, os_, 0, 0, K, int(bool(silu)), code)
         _check(get_lib().ssm_conv1d_fwd(px, pw, pb, pc, pwin if K > 1 else None, ps, ph, po, ctypes.byref(dims), sp))
     return out
@@ -197,7 +204,7 @@ def ssm_conv1d_step(windows, x, conv_w, conv_bias, slots=None, silu=True, out=No
     act, f32 = x.dtype, torch.float32
     code = _act_code(x)
     K = int(conv_w.shape[1])
-    px, xs = _rows(x, device=dev, name="x")
+    px, xs = _rows(x, dev, "x")
     pw = _flat(conv_w, f32, dev, (dim, K), "conv_w")
     pb = _flat(conv_bias, f32, dev, (dim,), "conv_bias")
     ps = _flat(slots, torch.int32, dev, (b,), "slots")
@@ -205,8 +212,8 @@ def ssm_conv1d_step(windows, x, conv_w, conv_bias, slots=None, silu=True, out=No
     pwin = _flat(windows, act, dev, (nslots, K - 1, dim), "windows")
     with _on(dev, stream) as sp:
         if out is None:
-            out = torch.empty((b, dim), dtype=act, device=dev)
-        po, os_ = _rows(out, dtype=act, device=dev, shape=(b, dim), name="out")
+            out = _like(x)
+        po, os_ = _rows(out, dev, "out", act, (b, dim))
         dims = Conv1dDims(b, dim, 0, nslots, xs, os_, 0, 0, K, int(bool(silu)), code)
         _check(get_lib().ssm_conv1d_step(pwin if K > 1 else None, ps, px, pw, pb, po, ctypes.byref(dims), sp))
     return out
@@ -221,17 +228,17 @@ def ssm_conv1d_bwd(x, conv_w, conv_bias, cu_seqlens, dy, silu=True, dx=None, str
     act, f32 = x.dtype, torch.float32
     code = _act_code(x)
     K = int(conv_w.shape[1])
-    px, xs = _rows(x, device=dev, name="x")
+    px, xs = _rows(x, dev, "x")
     pw = _flat(conv_w, f32, dev, (dim, K), "conv_w")
     pb = _flat(conv_bias, f32, dev, (dim,), "conv_bias")
     pc, _, _, n = _tables(cu_seqlens, None, None, dev)
-    pdy, dys = _rows(dy, dtype=act, device=dev, shape=(T, dim), name="dy")
+    pdy, dys = _rows(dy, dev, "dy", act, (T, dim))
     with _on(dev, stream) as sp:
         if dx is None:
-            dx = torch.empty((T, dim), dtype=act, device=dev)
-        pdx, dxs = _rows(dx, dtype=act, device=dev, shape=(T, dim), name="dx")
-        dw = torch.empty((dim, K), dtype=f32, device=dev)
-        dbias = torch.empty(dim, dtype=f32, device=dev) if conv_bias is not None else None
+            dx = _like(x)
+        pdx, dxs = _rows(dx, dev, "dx", act, (T, dim))
+        dw = _like(conv_w)
+        dbias = _like(conv_bias) if conv_bias is not None else None
         dims = Conv1dDims(T, dim, n, 0, xs, 0, dys, dxs, K, int(bool(silu)), code)
         lib = get_lib()
         pws, nws, _keep = _workspace(lib.ssm_conv1d_bwd_workspace_size, dims, workspace, dev)
@@ -248,10 +255,10 @@ def _ssd_args(x, dt, dt_bias, A, B, C, D, dev):
         if not isinstance(t, torch.Tensor) or t.dim() != 3:
             raise ValueError(f"{name} must be [rows, groups, {DSTATE_SSD}]")
     G, N = B.shape[1], B.shape[2]
-    px, xs = _rows(x, device=dev, name="x")
-    pdt, dts = _rows(dt, dtype=act, device=dev, shape=(T, H), name="dt")
-    pB, bs = _rows(B, dtype=act, device=dev, shape=(T, G, N), name="B")
-    pC, cs = _rows(C, dtype=act, device=dev, shape=(T, G, N), name="C")
+    px, xs = _rows(x, dev, "x")
+    pdt, dts = _rows(dt, dev, "dt", act, (T, H))
+    pB, bs = _rows(B, dev, "B", act, (T, G, N))
+    pC, cs = _rows(C, dev, "C", act, (T, G, N))
     pbias = _flat(dt_bias, f32, dev, (H,), "dt_bias")
     pA = _flat(A, f32, dev, (H,), "A")
     pD = _flat(D, f32, dev, (H,), "D")
@@ -279,8 +286,8 @@ def ssm_ssd_varlen_fwd(x, dt, dt_bias, softplus, A, B, C, D, cu_seqlens, states=
     lib = get_lib()
     with _on(dev, stream) as sp:
         if out is None:
-            out = torch.empty(tuple(x.shape), dtype=x.dtype, device=dev)
-        po, dims.y_stride = _rows(out, dtype=x.dtype, device=dev, shape=x.shape, name="out")
+            out = _like(x)
+        po, dims.y_stride = _rows(out, dev, "out", x.dtype, x.shape)
         pws, nws, _keep = _workspace(lib.ssm_ssd_varlen_fwd_workspace_size, dims, workspace, dev)
         _check(lib.ssm_ssd_varlen_fwd(px, pdt, pbias, int(bool(softplus)), pA, pB, pC, pD, pc, pst, ps, ph, po, pws, nws,
                                       ctypes.byref(dims), sp))
@@ -304,8 +311,8 @@ def ssm_ssd_step(states, x, dt, dt_bias, softplus, A, B, C, D=None, slots=None, 
     ps = _flat(slots, torch.int32, dev, (x.shape[0],), "slots")
     with _on(dev, stream) as sp:
         if out is None:
-            out = torch.empty(tuple(x.shape), dtype=x.dtype, device=dev)
-        po, dims.y_stride = _rows(out, dtype=x.dtype, device=dev, shape=x.shape, name="out")
+            out = _like(x)
+        po, dims.y_stride = _rows(out, dev, "out", x.dtype, x.shape)
         _check(get_lib().ssm_ssd_step(pst, ps, px, pdt, pbias, int(bool(softplus)), pA, pB, pC, pD, po,
                                       ctypes.byref(dims), sp))
     return out
@@ -314,8 +321,8 @@ def ssm_ssd_step(states, x, dt, dt_bias, softplus, A, B, C, D=None, slots=None, 
 def _norm_args(x, weight, z, groups, eps, gate_first):
     dev = _cuda(x, 2, "x")
     rows, dim = x.shape
-    px, xs = _rows(x, device=dev, name="x")
-    pz, zs = _rows(z, dtype=x.dtype, device=dev, shape=x.shape, name="z")
+    px, xs = _rows(x, dev, "x")
+    pz, zs = _rows(z, dev, "z", x.dtype, x.shape)
     pw = _flat(weight, torch.float32, dev, (dim,), "weight")
     dims = NormDims(rows, dim, int(groups), xs, zs, 0, 0, 0, 0, float(eps), int(bool(gate_first)), _act_code(x))
     return dev, px, pz, pw, dims
@@ -329,8 +336,8 @@ def ssm_gated_norm_fwd(x, weight, z=None, groups=1, eps=1e-5, gate_first=True, o
     dev, px, pz, pw, dims = _norm_args(x, weight, z, groups, eps, gate_first)
     with _on(dev, stream) as sp:
         if out is None:
-            out = torch.empty(tuple(x.shape), dtype=x.dtype, device=dev)
-        po, dims.out_stride = _rows(out, dtype=x.dtype, device=dev, shape=x.shape, name="out")
+            out = _like(x)
+        po, dims.out_stride = _rows(out, dev, "out", x.dtype, x.shape)
         rstd = torch.empty((x.shape[0], max(int(groups), 1)), dtype=torch.float32, device=dev)
         _check(get_lib().ssm_gated_norm_fwd(px, pz, pw, po, rstd.data_ptr(), ctypes.byref(dims), sp))
     return out, rstd
@@ -341,18 +348,18 @@ def ssm_gated_norm_bwd(x, weight, z, dout, groups=1, eps=1e-5, gate_first=True, 
     """Gradients of ssm_gated_norm_fwd given dout.  Returns a dict: dx and dz (None
     without z) in x's dtype, dweight [dim] float32."""
     dev, px, pz, pw, dims = _norm_args(x, weight, z, groups, eps, gate_first)
-    pd, dims.dout_stride = _rows(dout, dtype=x.dtype, device=dev, shape=x.shape, name="dout")
+    pd, dims.dout_stride = _rows(dout, dev, "dout", x.dtype, x.shape)
     lib = get_lib()
     with _on(dev, stream) as sp:
         if dx is None:
-            dx = torch.empty(tuple(x.shape), dtype=x.dtype, device=dev)
+            dx = _like(x)
         if z is None:
             dz = None
         elif dz is None:
-            dz = torch.empty(tuple(x.shape), dtype=x.dtype, device=dev)
-        pdx, dims.dx_stride = _rows(dx, dtype=x.dtype, device=dev, shape=x.shape, name="dx")
-        pdz, dims.dz_stride = _rows(dz, dtype=x.dtype, device=dev, shape=x.shape, name="dz")
-        dweight = torch.empty(x.shape[1], dtype=torch.float32, device=dev)
+            dz = _like(x)
+        pdx, dims.dx_stride = _rows(dx, dev, "dx", x.dtype, x.shape)
+        pdz, dims.dz_stride = _rows(dz, dev, "dz", x.dtype, x.shape)
+        dweight = _like(weight)
         pws, nws, _keep = _workspace(lib.ssm_gated_norm_bwd_workspace_size, dims, workspace, dev)
         _check(lib.ssm_gated_norm_bwd(px, pz, pw, pd, pdx, pdz, dweight.data_ptr(), pws, nws, ctypes.byref(dims), sp))
     return dict(dx=dx, dz=dz, dweight=dweight)

@@ -201,6 +201,27 @@ def test_python_refuses_cpu_tensors_and_wrong_ranks(m):
         m.ssm_ssd_varlen_fwd(x3, torch.zeros(4, 2), None, True, torch.zeros(2), torch.zeros(4, 1, 128), torch.zeros(4, 1, 128), None, cu)
 
 
+def test_python_refuses_a_stream_of_another_device():
+    from selective_state_space_38_b200.mamba2 import _on
+
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError):
+        _on(torch.device("cuda", 0), Stream())
+
+
+def test_workspace_sizes_of_more_than_the_operators_take(m):
+    """Sizes whose products would leave 64 bits are refused before they are formed."""
+    lib, n = m.get_lib(), ctypes.c_size_t(0)
+    big = 1 << 62
+    for query, make, fields in ((lib.ssm_conv1d_bwd_workspace_size, _conv_dims, ("tokens", "dim")),
+                                (lib.ssm_ssd_varlen_fwd_workspace_size, _ssd_dims, ("tokens", "sequences", "heads")),
+                                (lib.ssm_gated_norm_bwd_workspace_size, _norm_dims, ("rows", "dim"))):
+        for k in fields:
+            assert query(make(m, **{k: big}), ctypes.byref(n)) == 2, k
+
+
 def test_row_strides(m):
     from selective_state_space_38_b200.mamba2 import _rows
     t = torch.zeros(6, 40)
