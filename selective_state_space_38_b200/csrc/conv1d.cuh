@@ -148,6 +148,7 @@ struct ConvChannels {
 // grid: row tiles x channel blocks, the channel blocks of a tile next to each other
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(kConvThreads, 6) conv1d_fwd_kernel(const Conv1dParams p) {
+    release_next();
     using R = Row<T, V>;
     constexpr bool kAccurate = Act<T>::kBytes == 4;
     constexpr int kL = R::kL, kN = R::kN;
@@ -220,6 +221,7 @@ __global__ void __launch_bounds__(kConvThreads, 6) conv1d_fwd_kernel(const Conv1
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(kConvThreads) conv1d_window_kernel(const Conv1dParams p) {
     using R = Row<T, V>;
+    wait_previous();
     const int64_t c = (static_cast<int64_t>(blockIdx.x % p.cblocks) * kConvThreads + threadIdx.x) * V;
     if (c >= p.dim) return;
     {
@@ -286,6 +288,7 @@ __global__ void __launch_bounds__(kConvThreads) conv1d_step_kernel(const Conv1dP
 // not depend on the order in which blocks run.
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(kConvThreads, 4) conv1d_bwd_kernel(const Conv1dParams p) {
+    release_next();
     using R = Row<T, V>;
     constexpr bool kAccurate = Act<T>::kBytes == 4;
     constexpr int kL = R::kL, kN = R::kN, kB = kConvBwdBatch;
@@ -431,6 +434,7 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv1d_bwd_kernel(const Conv1
 __global__ void __launch_bounds__(256) conv1d_reduce_kernel(const float *partial, float *dw, float *dbias, int64_t dim,
                                                             int64_t tiles, int K) {
     __shared__ float part[8][32];
+    wait_previous();
     const int k = blockIdx.y;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
     float s = 0.0f;

@@ -121,6 +121,7 @@ __host__ __device__ constexpr int norm_bwd_smem(int threads, int nv, int bytes, 
 
 template <typename T, int V, int NV, bool GATE, bool GATE_FIRST, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) gated_norm_bwd_kernel(const NormParams p, int tpr) {
+    release_next();
     using R = Row<T, V>;
     constexpr bool kAccurate = Act<T>::kBytes == 4, kAsync = V * Act<T>::kBytes == 16;
     constexpr int kArrays = GATE ? 3 : 2, kStages = norm_stages(NV);
@@ -139,34 +140,64 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) gated_norm_bwd_kernel(const N
 #pragma unroll
         for (int e = 0; e < kN; ++e) dw[i][e] = lanes<kL>(0.0f);
     typename R::Raw reg[kAsync ? 1 : kArrays][kAsync ? 1 : NV];
-    // this thread's vector i of array a (x, dout, z) of trip k
-    auto at = [&](int64_t k, int a, int i) -> uint4 & {
-        return rows_smem[((static_cast<int>(k % kStages) * kArrays + a) * NV + i) * blockDim.x + threadIdx.x];
+    constexpr int kE = Act<T>::kBytes;
+    // the row's first vector of this thread, in each array; vector i is `apart` bytes times i on
+    const int64_t first = col0 + static_cast<int64_t>(j) * V;
+    const char *px = static_cast<const char *>(p.x) + (slot * p.x_stride + first) * kE;
+    const char *pd = static_cast<const char *>(p.dout) + (slot * p.dout_stride + first) * kE;
+    const char *pz = static_cast<const char *>(p.z) + (GATE ? (slot * p.z_stride + first) * kE : 0);
+    char *pdx = static_cast<char *>(p.dx) + (slot * p.dx_stride + first) * kE;
+    char *pdz = static_cast<char *>(p.dz) + (GATE ? (slot * p.dz_stride + first) * kE : 0);
+    const int64_t sx = step * p.x_stride * kE, sd = step * p.dout_stride * kE, sz = step * p.z_stride * kE,
+                  sdx = step * p.dx_stride * kE, sdz = step * p.dz_stride * kE;
+    const int apart = tpr * V * kE;
+    bool has[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) has[i] = (static_cast<int64_t>(i) * tpr + j) * V < p.gdim;
+    // the weights stay in registers where they fit
+    constexpr bool kKeep = NV * V <= 16;
+    float keep[kKeep ? NV : 1][V] = {};
+    if constexpr (kKeep) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (has[i]) load_params<V, (V > 1)>(p.weight + first + static_cast<int64_t>(i) * tpr * V, keep[i]);
+    }
+    auto weight = [&](int i, float (&w)[V]) {
+        if constexpr (kKeep) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) w[e] = keep[i][e];
+        } else {
+            if (has[i]) load_params<V, (V > 1)>(p.weight + first + static_cast<int64_t>(i) * tpr * V, w);
+        }
     };
-    auto load = [&](int64_t k) {
-        const int64_t row = slot + k * step;
+    // this thread's vector i of array a (x, dout, z) of a stage
+    auto at = [&](int stage, int a, int i) -> uint4 & { return rows_smem[((stage * kArrays + a) * NV + i) * blockDim.x + threadIdx.x]; };
+    auto load = [&](int stage, int64_t row) {  // the row that px, pd and pz are on; they move on
+        const bool in = row < p.rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t c = (static_cast<int64_t>(i) * tpr + j) * V;
-            const bool in = c < p.gdim && row < p.rows;
-            const int64_t ix = in ? row * p.x_stride + col0 + c : 0, id = in ? row * p.dout_stride + col0 + c : 0,
-                          iz = in ? row * p.z_stride + col0 + c : 0;
+            const bool some = in && has[i];
             if constexpr (kAsync) {
-                const uint32_t n = in ? 16u : 0u;
-                copy16_async(&at(k, 0, i), static_cast<const char *>(p.x) + ix * Act<T>::kBytes, n);
-                copy16_async(&at(k, 1, i), static_cast<const char *>(p.dout) + id * Act<T>::kBytes, n);
-                if constexpr (GATE) copy16_async(&at(k, 2, i), static_cast<const char *>(p.z) + iz * Act<T>::kBytes, n);
+                if (some) {
+                    copy16_async(&at(stage, 0, i), px + i * apart, 16);
+                    copy16_async(&at(stage, 1, i), pd + i * apart, 16);
+                    if constexpr (GATE) copy16_async(&at(stage, 2, i), pz + i * apart, 16);
+                } else {
+                    at(stage, 0, i) = at(stage, 1, i) = make_uint4(0, 0, 0, 0);
+                    if constexpr (GATE) at(stage, 2, i) = make_uint4(0, 0, 0, 0);
+                }
             } else {
-                reg[0][i] = in ? R::load_raw(p.x, ix) : R::zero_raw();
-                reg[1][i] = in ? R::load_raw(p.dout, id) : R::zero_raw();
-                if constexpr (GATE) reg[2][i] = in ? R::load_raw(p.z, iz) : R::zero_raw();
+                reg[0][i] = some ? R::load_raw(px + i * apart, 0) : R::zero_raw();
+                reg[1][i] = some ? R::load_raw(pd + i * apart, 0) : R::zero_raw();
+                if constexpr (GATE) reg[2][i] = some ? R::load_raw(pz + i * apart, 0) : R::zero_raw();
             }
         }
         if constexpr (kAsync) copy_async_commit();
+        px += sx, pd += sd, pz += sz;
     };
-    auto get = [&](int64_t k, int a, int i) -> typename R::Raw {
+    auto get = [&](int stage, int a, int i) -> typename R::Raw {
         if constexpr (kAsync) {
-            const uint4 v = at(k, a, i);
+            const uint4 v = at(stage, a, i);
             typename R::Raw r;
             r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
             return r;
@@ -174,20 +205,21 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) gated_norm_bwd_kernel(const N
             return reg[a][i];
         }
     };
-    const int64_t trips = (p.rows + step - 1) / step;  // the same for every thread: all join the sums
-    if constexpr (kAsync && kStages > 1) load(0);
-    for (int64_t k = 0; k < trips; ++k) {
-        const int64_t row = slot + k * step;
-        load(k + (kAsync ? kStages - 1 : 0));  // (past the last row: zeros, so that the count of groups stays)
-        if constexpr (kAsync) copy_async_wait<kStages - 1>();
+    const int trips = static_cast<int>((p.rows + step - 1) / step);  // the same for every thread: all join the sums
+    constexpr int kAhead = kAsync ? kStages - 1 : 0;
+    if constexpr (kAhead > 0) load(0, slot);
+    int64_t row = slot;
+    int st = 0;
+    for (int k = 0; k < trips; ++k, row += step, st = kStages - 1 - st, pdx += sdx, pdz += sdz) {
+        load(kAhead > 0 ? 1 - st : 0, row + kAhead * step);  // (past the last row: zeros, so that the count of groups stays)
+        if constexpr (kAsync) copy_async_wait<kAhead>();
         Ln sg[GATE ? NV : 1][kN];     // sigmoid(z)
         Ln ss2 = lanes<kL>(0.0f), dot2 = lanes<kL>(0.0f);  // sums of v^2, and of (up w) v
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t c = (static_cast<int64_t>(i) * tpr + j) * V;
             float w[V] = {};
-            if (c < p.gdim) load_params<V, (V > 1)>(p.weight + col0 + c, w);
-            const typename R::Raw cx = get(k, 0, i), cd = get(k, 1, i), cz = get(k, GATE ? 2 : 0, i);
+            weight(i, w);
+            const typename R::Raw cx = get(st, 0, i), cd = get(st, 1, i), cz = get(st, GATE ? 2 : 0, i);
 #pragma unroll
             for (int e = 0; e < kN; ++e) {
                 Ln v = R::pair(cx, e), up = R::pair(cd, e);
@@ -221,12 +253,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) gated_norm_bwd_kernel(const N
         if (row >= p.rows) continue;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t c = (static_cast<int64_t>(i) * tpr + j) * V;
-            if (c >= p.gdim) continue;
+            if (!has[i]) continue;
             float w[V];
             Ln dx[kN], dz[kN];
-            load_params<V, (V > 1)>(p.weight + col0 + c, w);
-            const typename R::Raw cx = get(k, 0, i), cd = get(k, 1, i), cz = get(k, GATE ? 2 : 0, i);
+            weight(i, w);
+            const typename R::Raw cx = get(st, 0, i), cd = get(st, 1, i), cz = get(st, GATE ? 2 : 0, i);
             const Ln r2 = lanes<kL>(r), m2 = lanes<kL>(-mean), one = lanes<kL>(1.0f);
 #pragma unroll
             for (int e = 0; e < kN; ++e) {
@@ -252,22 +283,23 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) gated_norm_bwd_kernel(const N
                     dx[e] = r2 * Ln::fma(n, m2, d * we);
                 }
             }
-            R::store(p.dx, row * p.dx_stride + col0 + c, dx);
-            if constexpr (GATE) R::store(p.dz, row * p.dz_stride + col0 + c, dz);
+            R::store(pdx + i * apart, 0, dx);
+            if constexpr (GATE) R::store(pdz + i * apart, 0, dz);
         }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int64_t c = (static_cast<int64_t>(i) * tpr + j) * V;
-        if (c >= p.gdim) continue;
+        if (!has[i]) continue;
+        const int64_t c = first + static_cast<int64_t>(i) * tpr * V;
 #pragma unroll
-        for (int e = 0; e < V; ++e) p.partial[slot * p.dim + col0 + c + e] = dw[i][e / kL].get(e % kL);
+        for (int e = 0; e < V; ++e) p.partial[slot * p.dim + c + e] = dw[i][e / kL].get(e % kL);
     }
 }
 
 // dweight[c] = sum over the slots of partial[slot][c], in a fixed order.  grid: dim / 32
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *partial, float *dweight, int64_t dim, int64_t slots) {
     __shared__ float part[32][33];
+    wait_previous();
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
     float s = 0.0f;
     if (c < dim) {

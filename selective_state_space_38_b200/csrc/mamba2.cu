@@ -115,6 +115,19 @@ int conv_dispatch(int32_t act_dtype, bool vec, int k, F f) {
 
 int launched() { return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA; }
 
+// A kernel whose blocks may come while the one before it on the stream still runs; it waits for
+// that one's end itself (wait_previous).
+template <typename... P, typename... A>
+bool launch_after(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaStream_t stream, const A &...args) {
+    cudaLaunchAttribute after;
+    after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    after.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid, cfg.blockDim = block, cfg.dynamicSmemBytes = static_cast<size_t>(smem), cfg.stream = stream;
+    cfg.attrs = &after, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
 // Rows of a tile.  A tile reads K - 1 rows before its own (and, for the gradients,
 // after them) and its taps again, so tiles are long; but few rows are cut shorter,
 // down to 16, until some four blocks of 128 threads stand for each SM.
@@ -168,8 +181,10 @@ int ssm_conv1d_fwd(const void *x, const float *w, const float *bias, const int32
         p.cblocks = conv_cblocks(p.dim, V);
         conv1d_fwd_kernel<T, V, k><<<static_cast<unsigned>(tiles * p.cblocks), kConvThreads, 0, s>>>(p);
         p.cblocks = conv_cblocks(p.dim, v);
-        if (windows && k > 1)
-            conv1d_window_kernel<T, v, k><<<static_cast<unsigned>(p.seq.sequences * static_cast<int64_t>(p.cblocks)), kConvThreads, 0, s>>>(p);
+        if (windows && k > 1 &&
+            !launch_after(conv1d_window_kernel<T, v, k>, dim3(static_cast<unsigned>(p.seq.sequences * static_cast<int64_t>(p.cblocks))),
+                          dim3(kConvThreads), 0, s, p))
+            return static_cast<int>(SSM_ERR_CUDA);
         return launched();
     });
 }
@@ -249,8 +264,11 @@ int ssm_conv1d_bwd(const void *x, const float *w, const float *bias, const int32
             p.cblocks = conv_cblocks(p.dim, V2);
             conv1d_bwd_kernel<decltype(t), V2, k><<<static_cast<unsigned>(tiles * p.cblocks), kConvThreads, 0, s>>>(p);
         }
-        conv1d_reduce_kernel<<<dim3(static_cast<unsigned>((p.dim + 31) / 32), k + 1), dim3(32, 8), 0, s>>>(
-            p.partial, p.dw, p.dbias, p.dim, tiles, k);
+        const float *partial = p.partial;
+        const int width = k;
+        if (!launch_after(conv1d_reduce_kernel, dim3(static_cast<unsigned>((p.dim + 31) / 32), k + 1), dim3(32, 8), 0, s, partial, p.dw,
+                          p.dbias, p.dim, tiles, width))
+            return static_cast<int>(SSM_ERR_CUDA);
         return launched();
     });
 }
@@ -418,11 +436,16 @@ int ssm_gated_norm_bwd(const void *x, const void *z, const float *weight, const 
             kernel<<<grid, threads, smem, st>>>(p, s.tpr);
             return SSM_OK;
         };
-        const int rc2 = nv * v <= 16 && threads <= 320
-                            ? launch(gated_norm_bwd_kernel<decltype(t), v, nv, gate, first, 320, 2>)
-                            : launch(gated_norm_bwd_kernel<decltype(t), v, nv, gate, first, kNormThreads, 1>);
+        int rc2 = -1;
+        if constexpr (nv * v <= 16) {
+            if (threads <= 320) rc2 = launch(gated_norm_bwd_kernel<decltype(t), v, nv, gate, first, 320, 2>);
+        }
+        if (rc2 < 0) rc2 = launch(gated_norm_bwd_kernel<decltype(t), v, nv, gate, first, kNormThreads, 1>);
         if (rc2 != SSM_OK) return rc2;
-        norm_reduce_kernel<<<static_cast<unsigned>((p.dim + 31) / 32), dim3(32, 32), 0, st>>>(p.partial, dweight, p.dim, blocks * s.rpb);
+        const float *partial = p.partial;
+        const int64_t slots = blocks * s.rpb;
+        if (!launch_after(norm_reduce_kernel, dim3(static_cast<unsigned>((p.dim + 31) / 32)), dim3(32, 32), 0, st, partial, dweight, p.dim, slots))
+            return static_cast<int>(SSM_ERR_CUDA);
         return launched();
     });
 }
@@ -512,19 +535,6 @@ size_t var_layout(const ssm_ssd_packed_dims_t *d, uint8_t *base, VarWork *w) {
         w->carry = reinterpret_cast<float *>(base + carry);
     }
     return at;
-}
-
-// A kernel whose blocks may come while the one before it on the stream still runs; it waits for
-// that one's end itself.
-template <typename... P, typename... A>
-bool launch_after(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaStream_t stream, const A &...args) {
-    cudaLaunchAttribute after;
-    after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    after.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid, cfg.blockDim = block, cfg.dynamicSmemBytes = static_cast<size_t>(smem), cfg.stream = stream;
-    cfg.attrs = &after, cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
 int ssd_varlen_impl(const void *x, const void *dt, const float *dt_bias, int softplus, const float *A, const void *B,

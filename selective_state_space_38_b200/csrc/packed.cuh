@@ -146,6 +146,13 @@ __device__ __forceinline__ void copy_async_wait() {  // until at most N groups a
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// The kernels of a call may follow each other by programmatic dependent launch: each lets
+// the next one's blocks come while it runs, and waits for the one before to be over (its
+// writes seen) before it reads anything of its.  Every block waits, also one with nothing
+// to do: the kernel after takes this one's end for the end of both.
+__device__ __forceinline__ void release_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // N consecutive float32 parameters: as 16-byte vectors when VEC (the host checks their
 // alignment with the rows'), else one by one.
 template <int N, bool VEC>

@@ -151,14 +151,8 @@ static_assert(VarSmem::kTotal <= 227 * 1024, "shared memory of the packed SSD ke
 // never start in the same window of `segment` tokens (those of one sequence are
 // `segment` apart, those of the next sequence start more than that behind its start),
 // so a window's index names one.  One block of 1024 threads.
-// The kernels of a call follow each other by programmatic dependent launch: each lets
-// the next one's blocks come while it runs, and waits for the one before to be over
-// (its writes seen) before it reads anything of its.
-__device__ __forceinline__ void var_release_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void var_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams p) {
-    var_release_next();
+    release_next();
     __shared__ int2 at[kVarMaxWindows];
     __shared__ uint32_t sums[32];
     __shared__ uint32_t later, several, filled, bad;
@@ -237,8 +231,8 @@ __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams 
 // The states at the segments' starts from the segments' own: S_{s+1} = exp(T_s) S_s
 // + E_s, in place.  grid: (heads x 8, sequences of more than one segment at most)
 __global__ void __launch_bounds__(256) ssd_varlen_combine_kernel(const VarParams p) {
-    var_release_next();
-    var_wait_previous();
+    release_next();
+    wait_previous();
     if ((*p.work.error & 4u) || *p.work.mode != kVarTwoPasses) return;
     const int h = blockIdx.x / 8;
     const int64_t e = (blockIdx.x % 8) * 256 + threadIdx.x;  // a 16-byte vector of the state
@@ -392,7 +386,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
 
     // (the first pass does not let the next kernels' blocks come while it has work to do:
     // beside it they cost it 7 %)
-    var_wait_previous();
+    wait_previous();
     // the swizzled tiles need 1024-byte alignment; a work list that was refused has no items
     if ((smem_u32(sm) & 1023u) != 0) {
         if (tid == 0) atomicOr(error, 2u);
