@@ -134,7 +134,9 @@ int ssm_scan_fwd(const void *x, const void *delta, const float *delta_bias, int 
  * `stream` to finish, then reads the call's error word from the workspace.
  * Returns SSM_OK, SSM_ERR_TIMEOUT when one of the call's bounded device waits
  * gave up (its out and h_last are then void; every wait is bounded, so the
- * kernels always end), or SSM_ERR_CUDA when the stream reports a CUDA error.
+ * kernels always end), SSM_ERR_INVALID_ARG when an ssm_ssd_varlen_fwd call found
+ * cu_seqlens not ascending within its tokens (it then wrote nothing), or
+ * SSM_ERR_CUDA when the stream reports a CUDA error.
  * workspace == NULL asks about the last ssm_scan_fwd_noalloc call on the
  * current device.  This call blocks the host; the forward calls never do.
  */
@@ -356,6 +358,8 @@ int ssm_ssd_fwd(const void *x, const void *dt, const float *dt_bias, int softplu
  *   has_initial    optional [sequences] bytes on the device: non-zero where the
  *                  sequence goes on from its cache row (NULL: every sequence
  *                  starts from zeros).
+ * Workspaces are scratch of one call: calls that overlap on the GPU (two streams,
+ * two captured graphs that are replayed at once) need one each.
  * The cache row of a sequence that is not empty is updated in place.  An empty
  * sequence leaves its cache row as it was.  Values outside these ranges in the
  * device tables never lead to an access out of range.
@@ -455,10 +459,13 @@ int ssm_conv1d_bwd(const void *x, const float *w, const float *bias, const int32
  *                  within [0, tokens] (the call then wrote nothing)
  * Alignment: x, B, C, y, states and workspace 16 bytes, and the strides of x, B,
  * C and y multiples of 8 elements; dt its element size.  A value that is not
- * finite in a sequence may spread to the 128 steps around it.  Sequences of more
- * than 1024 tokens are walked in segments of 1024 (more when tokens exceed 2^20)
- * that may run on different SMs, the state passing through the workspace; results
- * do not depend on that.
+ * finite in a sequence may spread to the 128 steps of it around there, and from
+ * there on with the state; other sequences never see it.  A sequence's chunks of 128
+ * steps start at its first token, whatever is packed before it.  A long sequence may
+ * be cut at chunk ends between SMs, its float32 state passing through the workspace;
+ * where few sequences leave SMs idle they are cut into segments whose own states are
+ * formed first and joined afterwards, which may change the last bits of a state.
+ * Equal calls on one GPU model give equal bits.
  */
 int ssm_ssd_varlen_fwd_workspace_size(const ssm_ssd_packed_dims_t *dims, size_t *bytes);
 int ssm_ssd_varlen_fwd(const void *x, const void *dt, const float *dt_bias, int softplus, const float *A,
@@ -557,10 +564,11 @@ int ssm_debug_ssd_flag_timeout(const void *x, const void *dt, const float *dt_bi
                                ssm_stream_t stream);
 
 /*
- * Test support, not part of the operation: ssm_ssd_varlen_fwd where every later
- * segment of a sequence waits for a hand-off flag value that no flag ever reaches
- * and gives up after `spin_limit` polls (0: at once).  The kernel still ends
- * normally; ssm_scan_fwd_status then reports SSM_ERR_TIMEOUT.
+ * Test support, not part of the operation: ssm_ssd_varlen_fwd where every CTA whose
+ * share of the work begins inside a sequence waits for a hand-off flag value that no
+ * flag ever reaches and gives up after `spin_limit` polls (0: at once).  Only a call
+ * with such a share waits at all.  The kernel still ends normally;
+ * ssm_scan_fwd_status then reports SSM_ERR_TIMEOUT.
  */
 int ssm_debug_ssd_varlen_flag_timeout(const void *x, const void *dt, const float *dt_bias, int softplus,
                                       const float *A, const void *B, const void *C, const float *D,
