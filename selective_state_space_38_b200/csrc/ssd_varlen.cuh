@@ -132,11 +132,13 @@ struct VarChunk {
 
 struct VarSmem {
     static constexpr int kTile = 128 * 128;           // [128 rows][64] bf16, 128-byte swizzle
-    static constexpr int kC = 0, kB = 2 * kTile;      // [t][n]: n < 64, n >= 64
-    static constexpr int kX = 4 * kTile;              // [t][p] of each head; y passes through it
-    static constexpr int kXp = 6 * kTile;             // w x: parts x heads tiles
-    static constexpr int kS = kXp + kVarParts * kVarHeads * kTile;  // S [n][p] of each head
-    static constexpr int kTabD = kS + kVarHeads * kTile;            // d [head][128]
+    static constexpr int kC = 0;                      // [t][n]: n < 64, n >= 64
+    static constexpr int kB = 2 * kTile, kBufB = 2 * kTile;  // the same, of even and of odd chunks
+    static constexpr int kX = kB + 2 * kBufB;         // [t][p] of each head; y passes through it
+    static constexpr int kXp = kX + kVarHeads * kTile;  // w x: parts x heads tiles
+    // S [n][p] of each head, in the last part's place: C S has read it before the parts are formed
+    static constexpr int kS = kXp + (kVarParts - 1) * kVarHeads * kTile;
+    static constexpr int kTabD = kXp + kVarParts * kVarHeads * kTile;  // d [head][128]
     static constexpr int kTabW = kTabD + kVarHeads * 512;           // w where the factors are in range, else dt
     static constexpr int kInfo = kTabW + kVarHeads * 512;           // of even and of odd chunks
     static constexpr int kItem = kInfo + 256;
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     if (SUMMARY && mode != kVarTwoPasses) return;
     if (tid == 0) {
         for (int i = 0; i < 15; ++i) {
-            const uint32_t n = i < 8 ? 1 : i == 8 ? (SUMMARY ? 1 : 2) : i == 9 ? 2 * kVarHalf + 2 : i == 13 ? 2 * kVarHalf : i < 13 ? kStateThreads : kVarHalf;
+            const uint32_t n = i < 9 ? 1 : i == 9 ? 2 * kVarHalf + 2 : i == 13 ? 2 * kVarHalf : i < 13 ? kStateThreads : kVarHalf;
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar + i)), "r"(n));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                        aXp = smem_u32(sm + S::kXp), aS = smem_u32(sm + S::kS);
         uint32_t nG = 0, nC = 0, nS = 0, nY = 0;  // issued
         for (uint32_t u = 0;; ++u) {
-            const uint32_t ph = u & 1u, tYu = tY + 128 * ph;
+            const uint32_t ph = u & 1u, tYu = tY + 128 * ph, aBu = aB + S::kBufB * ph;
             if (!wait(bFull, ph)) break;
             const int heads = info[ph].nh;
             const bool stop = info[ph].stop;
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             if constexpr (!SUMMARY) {
                 if (ssd_elect()) {  // C B^T
                     constexpr uint32_t id = ssd_idesc(128, 128, 0, 0);
-                    const uint64_t dC = ssd_desc(aC, 16, 1024), dB = ssd_desc(aB, 16, 1024);
+                    const uint64_t dC = ssd_desc(aC, 16, 1024), dB = ssd_desc(aBu, 16, 1024);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const uint32_t o = ((k / 4) * S::kTile + (k % 4) * 32) >> 4;
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     if (ssd_elect()) {  // S += B^T (w x), the smallest part first
                         constexpr uint32_t id = ssd_idesc(128, kN, 1, 1);
-                        const uint64_t dB = ssd_desc(aB, S::kTile, 1024), dX = ssd_desc(aXp, S::kTile, 1024);
+                        const uint64_t dB = ssd_desc(aBu, S::kTile, 1024), dX = ssd_desc(aXp, S::kTile, 1024);
 #pragma unroll
                         for (int part = kVarParts - 1; part >= 0; --part)
 #pragma unroll
@@ -513,10 +515,10 @@ __global__ void __launch_bounds__(kVarThreads, 1)
         if (nY > 0) ssd_drain(mY, (nY - 1) & 1u, error);
         __syncwarp();
     } else if (warp == kLoadWarp) {
-        // ---- the loads: C once C S has read the chunk's before, B once its state's products
-        // have, X once the state's warps have and y, which passes through it, is out of it ---
-        uint32_t nX = 0, nCB = 0;  // issued in full
-        bool half = false;         // C is on its way without B
+        // ---- the loads: C once C S has read the chunk's before, and B with it (its buffer is
+        // free: that C S had the state after the products that read it); X once the state's
+        // warps have read the one before and y, which passes through it, is out of it ---------
+        uint32_t nX = 0, nCB = 0;  // issued
         for (uint32_t u = 0;; ++u) {
             const uint32_t ph = u & 1u, pv = ph ^ 1u;
             if (!wait(bFull, ph)) break;
@@ -525,26 +527,21 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             __syncwarp();
             if (lane == 0) ssd_arrive(bEmpty);
             if (stop) break;
-            bool c = SUMMARY, b = false, x = false;
-            for (uint32_t n = 0; !(c && b && x) && !give_up(n); ++n) {
-                if (!SUMMARY && !c && (u == 0 || test(mC, pv))) {
+            bool cb = false, x = false;
+            for (uint32_t n = 0; !(cb && x) && !give_up(n); ++n) {
+                if (!cb && (u == 0 || test(SUMMARY ? mS : mC, pv))) {
                     if (ssd_elect()) {
-                        mbar_arrive_expect_tx(bCB, 2 * S::kTile);
-                        tma_load_3d(sm + S::kC, &tm.C, 0, g, t0, bCB);
-                        tma_load_3d(sm + S::kC + S::kTile, &tm.C, 64, g, t0, bCB);
+                        uint8_t *b = sm + S::kB + S::kBufB * ph;
+                        mbar_arrive_expect_tx(bCB, (SUMMARY ? 2 : 4) * S::kTile);
+                        if constexpr (!SUMMARY) {
+                            tma_load_3d(sm + S::kC, &tm.C, 0, g, t0, bCB);
+                            tma_load_3d(sm + S::kC + S::kTile, &tm.C, 64, g, t0, bCB);
+                        }
+                        tma_load_3d(b, &tm.B, 0, g, t0, bCB);
+                        tma_load_3d(b + S::kTile, &tm.B, 64, g, t0, bCB);
                     }
                     __syncwarp();
-                    c = half = true;
-                }
-                if (!b && c && (u == 0 || test(mS, pv))) {
-                    if (ssd_elect()) {
-                        mbar_arrive_expect_tx(bCB, 2 * S::kTile);
-                        tma_load_3d(sm + S::kB, &tm.B, 0, g, t0, bCB);
-                        tma_load_3d(sm + S::kB + S::kTile, &tm.B, 64, g, t0, bCB);
-                    }
-                    __syncwarp();
-                    b = true;
-                    half = false;
+                    cb = true;
                     ++nCB;
                 }
                 if (!x && (u == 0 || (test(bE1, pv) && (SUMMARY || test(bYf, pv))))) {
@@ -557,14 +554,9 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                     ++nX;
                 }
             }
-            if (!(c && b && x)) break;
+            if (!(cb && x)) break;
         }
-        // nothing in flight when the CTA ends: a C without its B is let land by completing
-        // the barrier's arrivals
-        if (half) {
-            if (lane == 0) ssd_arrive(bCB);
-            ++nCB;
-        }
+        // nothing in flight when the CTA ends
         if (nX > 0) ssd_drain(bX, (nX - 1) & 1u, error);
         if (nCB > 0) ssd_drain(bCB, (nCB - 1) & 1u, error);
         __syncwarp();
@@ -912,6 +904,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             // w x as three bf16 parts; rows past the chunk's end are zeros whatever they hold
             // (another sequence's values, or none)
             if (!wait(bX, ph)) break;
+            if (!SUMMARY && !wait(mC, ph)) break;  // S read: the last part takes its place
             const bool in = row < rows && live;
             const L2 w2 = lanes<2>(w), minus = lanes<2>(-1.0f);
 #pragma unroll 1
@@ -938,11 +931,13 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             }
             // B's rows past the end meet zeros, but a NaN there would not vanish
             if (rows < kVarQ) {
-                if (!wait(bCB, ph)) break;
+                // (with outputs C B^T was waited for, and the next chunk's B may have landed: a wait
+                // for this one's could not tell them apart)
+                if (SUMMARY && !wait(bCB, ph)) break;
                 if (row >= rows) {
 #pragma unroll
                     for (int k = c0 / 8; k < (c0 + kCols) / 8; ++k)
-                        *reinterpret_cast<uint4 *>(sm + S::kB + head * S::kTile + ssd_sw128(row, 8 * k)) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(sm + S::kB + S::kBufB * ph + head * S::kTile + ssd_sw128(row, 8 * k)) = make_uint4(0, 0, 0, 0);
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
