@@ -17,8 +17,12 @@
 // to the largest and counts a masked zero as 2^-126 times its x: with x scaled over
 // e^110 the first rows of a chunk came out wrong by their whole value.)  Where |d|
 // passes kVarRange the factors would leave bfloat16's range: there the matrix takes
-// its decays element by element against a row factor exp(cs_i), held to e^-70 at
-// least, and S comes unscaled.  The state accumulates in tensor memory on exp(T) S.
+// its decays against a row factor exp(cs_i), held to e^-70 at least, and S comes
+// unscaled.  Its decays are then, for a block of 16 columns from j0 on, one factor of
+// the row, exp(c_i - d_j0), times w_j = exp(d_j0 - d_j) dt_j, or, where d moves by more
+// than kVarSpan within 16 steps, formed one by one.  (One by one throughout, the heads
+// of such decays took 1.25 times the others' time, and at 4 x 4096 their CTAs 220 us
+// where the median took 180.)  The state accumulates in tensor memory on exp(T) S.
 //
 // Roundings to bf16 are those of the tensor core's operands: C B^T with its factors
 // once, S once where it meets C (each at most the half step that y's own rounding
@@ -31,8 +35,8 @@
 // shared memory carries about 640 KB for them and their operands, 5000 cycles at
 // 128 bytes a cycle, and bounds it together with the chain from a chunk's state to the
 // next one's (about 8600 cycles are measured).  4 x 4096 tokens of 80 heads in one
-// group take 212 us: 307 TFLOP/s, 18 % of the dense rate, 1.7 TB/s; 20 ragged prompts
-// of 24 heads 82 us; one of 32768 tokens and 24 heads 215 us.  One CTA per SM.  One warp issues the TMA loads and one the MMAs,
+// group take 190 us: 342 TFLOP/s, 20 % of the dense rate, 1.9 TB/s; 20 ragged prompts
+// of 24 heads 81 us; one of 32768 tokens and 24 heads 209 us.  One CTA per SM.  One warp issues the TMA loads and one the MMAs,
 // one walks the work list, one forms the chunks' running sums and factors, and
 // sixteen epilogue warps work in two halves: eight on the state (S and its operand,
 // the parts of w x), eight on the output (y), so that a chunk's y is written while the
@@ -64,6 +68,7 @@ constexpr int kVarQ = 128;          // steps of a chunk at most
 constexpr int kVarMaxWindows = 1024;
 constexpr int kVarMaxCtas = 160;
 constexpr float kVarRange = 70.0f;
+constexpr float kVarSpan = 40.0f;  // e^40 and e^-87 keep the products of a block's factors well inside float32
 constexpr int kVarHalf = 256;       // epilogue threads on the state, and on the output
 constexpr int kVarThreads = 2 * kVarHalf + 128;  // + a warp for the MMAs, the tables, the loads and the work list each
 constexpr int kVarHeads = 2;        // heads walked together
@@ -119,6 +124,9 @@ struct VarItem {
     float A[2], bias[2], D[2];
 };
 
+// How C B^T takes a head's decays: by columns, by rows and columns of 16-column blocks, one by one.
+enum VarDecays : int32_t { kVarByColumn = 0, kVarByBlock = 1, kVarOneByOne = 2 };
+
 // What the table warp hands on with each chunk.
 struct VarChunk {
     int32_t t0, rows;        // first token, steps
@@ -129,8 +137,8 @@ struct VarChunk {
     float *dst;
     uint32_t *flag;
     float decay[2], scale[2], D[2];  // exp(T); of S where it meets C
-    float ref[2];            // cs - ref is the row factor's exponent where the decays are taken one by one
-    int32_t factored[2];
+    float ref[2];            // T: cs = d + T, the row factor's exponent where the decays are not by columns
+    int32_t decays[2];       // VarDecays
 };
 
 struct VarSmem {
@@ -142,7 +150,7 @@ struct VarSmem {
     // S [n][p] of each head, in the last part's place: C S has read it before the parts are formed
     static constexpr int kS = kXp + (kVarParts - 1) * kVarHeads * kTile;
     static constexpr int kTabD = kXp + kVarParts * kVarHeads * kTile;  // d [head][128]
-    static constexpr int kTabW = kTabD + kVarHeads * 512;           // w where the factors are in range, else dt
+    static constexpr int kTabW = kTabD + kVarHeads * 512;           // the columns' factors (with decays one by one: dt)
     static constexpr int kInfo = kTabW + kVarHeads * 512;           // of even and of odd chunks
     static constexpr int kItem = kInfo + 256;
     static constexpr int kBar = kItem + 128;
@@ -220,7 +228,7 @@ __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams 
         *p.work.several = several;
         // In tenths of a chunk's time: a CTA's share, with six for the start and the end of each
         // chain; the two passes cost 1.4 times that, an uneven last segment, and their launches
-        // (four chunks' time).  Measured on 24 heads: one sequence of 32768 tokens 215 us in two
+        // (four chunks' time).  Measured on 24 heads: one sequence of 32768 tokens 209 us in two
         // passes against some 1300 as chains; 20 sequences, the longest of 2048, 82 against 134.
         const uint32_t share = (before + p.ctas - 1) / p.ctas;
         const int64_t each = (10ll * before + 6ll * filled * p.pairs) / p.ctas;
@@ -297,11 +305,11 @@ struct VarRange {
     }
 };
 
-// The exponent of a row's factor.  Where the decays are taken one by one it is cs_i,
+// The exponent of a row's factor.  Where the decays are not taken by columns it is cs_i,
 // held to [-70, 85] (beyond, only the state before the chunk would feel it, by e^-70
 // of itself; growth by e^85 overflows), and the rest is left to the matrix.
 __device__ __forceinline__ float var_row_exponent(const VarChunk &c, int i, float di) {
-    return c.factored[i] ? di : fminf(fmaxf(di + c.ref[i], -kVarRange), 85.0f);
+    return c.decays[i] == kVarByColumn ? di : fminf(fmaxf(di + c.ref[i], -kVarRange), 85.0f);
 }
 
 // C B^T with the factors of both heads, as bf16, over its own columns: of this warp's
@@ -328,12 +336,18 @@ __device__ __noinline__ void var_factors(const VarChunk &c, const float *tabD, c
         for (int i = 0; i < kVarHeads; ++i) {
             uint32_t r[8] = {};
             const float4 *wj = reinterpret_cast<const float4 *>(tabW + i * kVarQ + j0);
-            if (some && c.factored[i]) {
+            if (some && c.decays[i] != kVarOneByOne) {
+                float rf = 1.0f;  // the row's factor of the block; none above the diagonal, where it may overflow
+                if (c.decays[i] == kVarByBlock) {
+                    const float di = tabD[i * kVarQ + row];
+                    rf = j0 <= row ? ex2_approx((di - var_row_exponent(c, i, di) - tabD[i * kVarQ + j0]) * kLog2e) : 0.0f;
+                }
+                const L2 rf2 = lanes<2>(rf);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float4 f = wj[k];
-                    const L2 lo = L2::of(v[4 * k], v[4 * k + 1]) * L2::of(f.x, f.y);
-                    const L2 hi = L2::of(v[4 * k + 2], v[4 * k + 3]) * L2::of(f.z, f.w);
+                    const L2 lo = L2::of(v[4 * k], v[4 * k + 1]) * rf2 * L2::of(f.x, f.y);
+                    const L2 hi = L2::of(v[4 * k + 2], v[4 * k + 3]) * rf2 * L2::of(f.z, f.w);
                     r[2 * k] = pack_bf16x2(lo.get(0), lo.get(1));
                     r[2 * k + 1] = pack_bf16x2(hi.get(0), hi.get(1));
                 }
@@ -760,16 +774,24 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             const float T = -__shfl_sync(0xffffffffu, sum, 0, 16);
             float later = __shfl_down_sync(0xffffffffu, sum, 1, 16);
             if (sub == 15) later = 0.0f;
-            float most = fabsf(T), w[8];
+            float most = fabsf(T), w[8], span = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 d[i] += later;
                 most = fmaxf(most, fabsf(d[i]));
-                w[i] = expf(-d[i]) * dt[i];
             }
+            const float block = __shfl_sync(0xffffffffu, d[0], lane & ~1);  // d of the first of these 16 rows
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            const bool factored = most <= kVarRange;
+            for (int i = 0; i < 8; ++i) span = fmaxf(span, fabsf(block - d[i]));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) {
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                span = fmaxf(span, __shfl_xor_sync(0xffffffffu, span, o));
+            }
+            const VarDecays decays = most <= kVarRange ? kVarByColumn : span <= kVarSpan ? kVarByBlock : kVarOneByOne;
+            const float from = decays == kVarByColumn ? 0.0f : block;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = decays == kVarOneByOne ? dt[i] : expf(from - d[i]) * dt[i];
             item_total = (first ? 0.0f : item_total) + T;
             if (!ready()) {
                 ok = false;
@@ -777,14 +799,11 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             }
             float4 *pd = reinterpret_cast<float4 *>(tabD + hh * kVarQ + 8 * sub), *pw = reinterpret_cast<float4 *>(tabW + hh * kVarQ + 8 * sub);
             pd[0] = make_float4(d[0], d[1], d[2], d[3]), pd[1] = make_float4(d[4], d[5], d[6], d[7]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (!factored) w[i] = dt[i];
             pw[0] = make_float4(w[0], w[1], w[2], w[3]), pw[1] = make_float4(w[4], w[5], w[6], w[7]);
             VarChunk *out = info + (u & 1u);
             if (sub == 0) {
-                out->decay[hh] = expf(T), out->scale[hh] = factored ? expf(T) : 1.0f, out->D[hh] = D;
-                out->ref[hh] = T, out->factored[hh] = factored;
+                out->decay[hh] = expf(T), out->scale[hh] = decays == kVarByColumn ? expf(T) : 1.0f, out->D[hh] = D;
+                out->ref[hh] = T, out->decays[hh] = decays;
                 if (SUMMARY && last && mine) decay[hh] = expf(item_total);
             }
             if (lane == 0) {
@@ -855,7 +874,8 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             const L2 decay = lanes<2>(c.decay[head]);
             const float scale = c.scale[head];
             float w = tabW[head * kVarQ + row];
-            if (!c.factored[head]) w *= expf(-tabD[head * kVarQ + row]);
+            if (c.decays[head] != kVarByColumn)  // what is missing of exp(-d) dt
+                w *= expf(-tabD[head * kVarQ + (c.decays[head] == kVarByBlock ? row & ~15 : row)]);
             if constexpr (SUMMARY) ssd_arrive(bEmpty);
 
             // exp(T) S, float32, to tensor memory; S, scaled as it meets C, as bf16 to its

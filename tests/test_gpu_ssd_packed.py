@@ -114,6 +114,23 @@ def test_equal_decay_of_both_heads(rate):
     _check(inp, lens, initial=[True], what=f"rate {rate}")
 
 
+@pytest.mark.parametrize("rates", [(0.01, 1.0), (1.0, 0.01), (1.0, 4.0), (4.0, 0.01), (2.4, 2.6)])
+def test_decays_of_a_pair_of_different_kinds(rates):
+    """The two heads of a pair decay by these rates a step: 128 steps of 0.01 span little, of 1 too much for factors of
+    the columns alone, of 4 too much for factors of 16 columns; 16 of 2.4 and 2.6 lie about their limit.  The second
+    sequence's steps vary fourfold, and some are next to nothing."""
+    lens = [260, 140]
+    inp = ref.ssd_inputs(ref.gen(22), sum(lens), 2, 1)
+    steps = torch.full((sum(lens), 2), 0.1)
+    steps[260:] = 0.05 + 0.15 * torch.rand(140, 2, generator=ref.gen(23))
+    steps[270:275] = 1e-6
+    inp["dt"] = torch.log(torch.expm1(steps)).to(torch.bfloat16)
+    inp["dt_bias"] = None
+    inp["A"] = torch.tensor([-10.0 * r for r in rates])
+    inp["D"] = None
+    _check(inp, lens, initial=[True, True], what=f"rates {rates}")
+
+
 def test_without_bias_skip_and_softplus():
     lens = [150]
     inp = ref.ssd_inputs(ref.gen(12), 150, 2, 1)
