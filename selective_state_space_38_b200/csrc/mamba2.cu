@@ -284,7 +284,8 @@ namespace {
 
 constexpr int kNormThreads = 512;      // threads that share a row's group at most
 constexpr int kNormSmallBlock = 128;   // threads of a block whose rows need one warp or less
-constexpr int kNormBwdBlocks = 296;    // blocks of the gradient kernel in all: two for each of 148 SMs
+// blocks of the gradient kernel in all: two for each of 148 SMs (592: 186 us against 181 for 16384 rows of 5120)
+constexpr int kNormBwdBlocks = 296;
 
 // How the threads share a row's group of `gdim` columns: vectors of V elements,
 // NV to a thread, `tpr` threads.
@@ -431,7 +432,8 @@ int ssm_gated_norm_bwd(const void *x, const void *z, const float *weight, const 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return norm_dispatch(dims->act_dtype, s, z != nullptr, dims->gate_first != 0, [&](auto t, auto v, auto nv, auto gate, auto first) {
         // 16 elements a thread fit the 96 registers with which two blocks of 320 threads share an SM
-        // (three at 64 registers spilled: 210 us against 191 for 16384 rows of 5120)
+        // (three at 64 registers spilled: 196 us against 181 for 16384 rows of 5120, before the weights
+        // stayed in registers)
         const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(p.groups));
         const int threads = s.tpr * s.rpb, smem = norm_bwd_smem(threads, nv, v * static_cast<int>(es), gate);
         auto launch = [&](auto kernel) {
@@ -498,7 +500,7 @@ int64_t var_pairs(const ssm_ssd_packed_dims_t *d) {
 // Tokens of a segment of the two passes: two to seven chunks, about three segments to each of 148
 // SMs (a segment costs about half a chunk more for its state, and the last ones should even out;
 // one sequence of 32768 with 24 heads: 219 us with seven chunks, 250 with four; 20 ragged ones: 85
-// with two, 118 with five); longer where a thousand segments or sixteen to each SM would not do,
+// with two, 118 with five, before the last changes to the kernel); longer where a thousand segments or sixteen to each SM would not do,
 // which bounds the states in the workspace.
 int64_t var_segment(const ssm_ssd_packed_dims_t *d) {
     const int64_t chunks = (d->tokens + kVarQ - 1) / kVarQ;
