@@ -599,7 +599,7 @@ int ssd_varlen_impl(const void *x, const void *dt, const float *dt_bias, int sof
         // about eight blocks to an SM at most: where there is nothing to join they cost what they are launched for
         const unsigned several = static_cast<unsigned>(
             std::min<int64_t>({dims->sequences, p.windows, std::max<int64_t>(1, 1184 / (H * 8))}));
-        if (!launch_after(ssd_varlen_kernel<true>, dim3(ctas), dim3(kVarThreads), VarSmem::kTotal, s, p, tm) ||
+        if (!launch_after(ssd_varlen_kernel<true>, dim3(ctas), dim3(kVarSummaryThreads), VarSmem::kTotal, s, p, tm) ||
             !launch_after(ssd_varlen_combine_kernel, dim3(static_cast<unsigned>(H) * 8, several), dim3(256), 0, s, p))
             return SSM_ERR_CUDA;
     }

@@ -36,7 +36,7 @@
 // 128 bytes a cycle, and bounds it together with the chain from a chunk's state to the
 // next one's (about 8600 cycles are measured).  4 x 4096 tokens of 80 heads in one
 // group take 190 us: 342 TFLOP/s, 20 % of the dense rate, 1.9 TB/s; 20 ragged prompts
-// of 24 heads 81 us; one of 32768 tokens and 24 heads 209 us.  One CTA per SM.  One warp issues the TMA loads and one the MMAs,
+// of 24 heads 81 us; one of 32768 tokens and 24 heads 193 us.  One CTA per SM.  One warp issues the TMA loads and one the MMAs,
 // one walks the work list, one forms the chunks' running sums and factors, and
 // sixteen epilogue warps work in two halves: eight on the state (S and its operand,
 // the parts of w x), eight on the output (y), so that a chunk's y is written while the
@@ -70,7 +70,10 @@ constexpr int kVarMaxCtas = 160;
 constexpr float kVarRange = 70.0f;
 constexpr float kVarSpan = 40.0f;  // e^40 and e^-87 keep the products of a block's factors well inside float32
 constexpr int kVarHalf = 256;       // epilogue threads on the state, and on the output
-constexpr int kVarThreads = 2 * kVarHalf + 128;  // + a warp for the MMAs, the tables, the loads and the work list each
+// + a warp for the MMAs, the tables, the loads and the work list each; the first of the two passes has
+// two for the tables, which bound it (in the other a 21st warp leaves 80 registers a thread: 210 us
+// against 190 for 4 x 4096)
+constexpr int kVarThreads = 2 * kVarHalf + 128, kVarSummaryThreads = kVarThreads + 32;
 constexpr int kVarHeads = 2;        // heads walked together
 constexpr int kVarParts = 3;        // bf16 parts of w x
 
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams 
         *p.work.several = several;
         // In tenths of a chunk's time: a CTA's share, with six for the start and the end of each
         // chain; the two passes cost 1.4 times that, an uneven last segment, and their launches
-        // (four chunks' time).  Measured on 24 heads: one sequence of 32768 tokens 209 us in two
+        // (four chunks' time).  Measured on 24 heads: one sequence of 32768 tokens 193 us in two
         // passes against some 1300 as chains; 20 sequences, the longest of 2048, 82 against 134.
         const uint32_t share = (before + p.ctas - 1) / p.ctas;
         const int64_t each = (10ll * before + 6ll * filled * p.pairs) / p.ctas;
@@ -381,11 +384,12 @@ __device__ __noinline__ bool var_wait(uint64_t *bar, uint32_t parity, uint32_t *
 // SUMMARY: the first of the two passes, which forms the segments' own states only;
 // nothing to do when the setup kernel chose the ranges.
 template <bool SUMMARY>
-__global__ void __launch_bounds__(kVarThreads, 1)
+__global__ void __launch_bounds__(SUMMARY ? kVarSummaryThreads : kVarThreads, 1)
     ssd_varlen_kernel(const VarParams p, const __grid_constant__ VarMaps tm) {
     extern __shared__ __align__(1024) uint8_t var_smem[];
     using S = VarSmem;
     // without outputs all sixteen epilogue warps work on the state, half the columns each
+    constexpr int kTables = SUMMARY ? 2 : 1;  // warps on the tables
     constexpr int kStateThreads = SUMMARY ? 2 * kVarHalf : kVarHalf, kCols = SUMMARY ? 32 : 64;
     uint8_t *sm = var_smem;
     float *tabD = reinterpret_cast<float *>(sm + S::kTabD), *tabW = reinterpret_cast<float *>(sm + S::kTabW);
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     if (SUMMARY && mode != kVarTwoPasses) return;
     if (tid == 0) {
         for (int i = 0; i < 15; ++i) {
-            const uint32_t n = i < 9 ? 1 : i == 9 ? 2 * kVarHalf + 2 : i == 13 ? 2 * kVarHalf : i < 13 ? kStateThreads : kVarHalf;
+            const uint32_t n = i == 0 || i == 7 ? kTables : i < 9 ? 1 : i == 9 ? 2 * kVarHalf + 2 : i == 13 ? 2 * kVarHalf : i < 13 ? kStateThreads : kVarHalf;
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar + i)), "r"(n));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -442,7 +446,8 @@ __global__ void __launch_bounds__(kVarThreads, 1)
         if (n >= kSsdWaitLimit && lane == 0) atomicOr(error, 2u);
         return n >= kSsdWaitLimit || ((n & 1023u) == 1023u && __any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(error) != 0));
     };
-    constexpr int kMmaWarp = 2 * kVarHalf / 32, kTableWarp = kMmaWarp + 1, kLoadWarp = kMmaWarp + 2, kListWarp = kMmaWarp + 3;
+    constexpr int kMmaWarp = 2 * kVarHalf / 32, kTableWarp = kMmaWarp + 1,
+                  kLoadWarp = kTableWarp + kTables, kListWarp = kLoadWarp + 1;
     if (warp == kMmaWarp) {
         // ---- the products, issued by one elected lane -----------------------------------
         const uint32_t aC = smem_u32(sm + S::kC), aB = smem_u32(sm + S::kB), aX = smem_u32(sm + S::kX),
@@ -454,9 +459,12 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             const int heads = info[ph].nh;
             const bool stop = info[ph].stop;
             __syncwarp();
-            if (lane == 0) ssd_arrive(bEmpty);
+            if (!SUMMARY && lane == 0) ssd_arrive(bEmpty);
             // (the products before have read what C B^T replaces: mY)
             if (stop || !wait(bCB, ph) || (!SUMMARY && u > 0 && !wait(mY, ph ^ 1u))) break;
+            // (in the first pass the next chunk's B may come from here on, which a later wait for this
+            // one's could not tell apart)
+            if (SUMMARY && lane == 0) ssd_arrive(bEmpty);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             if constexpr (!SUMMARY) {
                 if (ssd_elect()) {  // C B^T
@@ -534,7 +542,9 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     } else if (warp == kLoadWarp) {
         // ---- the loads: C once C S has read the chunk's before, and B with it (its buffer is
         // free: that C S had the state after the products that read it); X once the state's
-        // warps have read the one before and y, which passes through it, is out of it ---------
+        // warps have read the one before and y, which passes through it, is out of it.  In the
+        // first pass B comes with X: the state's warps had waited for the products two chunks
+        // before, and the MMA warp has seen the B before land (bEmpty, then bFull) -------------
         uint32_t nX = 0, nCB = 0;  // issued
         for (uint32_t u = 0;; ++u) {
             const uint32_t ph = u & 1u, pv = ph ^ 1u;
@@ -546,7 +556,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             if (stop) break;
             bool cb = false, x = false;
             for (uint32_t n = 0; !(cb && x) && !give_up(n); ++n) {
-                if (!cb && (u == 0 || test(SUMMARY ? mS : mC, pv))) {
+                if (!cb && (u == 0 || test(SUMMARY ? bE1 : mC, pv))) {
                     if (ssd_elect()) {
                         uint8_t *b = sm + S::kB + S::kBufB * ph;
                         mbar_arrive_expect_tx(bCB, (SUMMARY ? 2 : 4) * S::kTile);
@@ -561,7 +571,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
                     cb = true;
                     ++nCB;
                 }
-                if (!x && (u == 0 || (test(bE1, pv) && (SUMMARY || test(bYf, pv))))) {
+                if (!x && (u == 0 || (SUMMARY ? cb : test(bE1, pv) && test(bYf, pv)))) {
                     if (ssd_elect()) {
                         mbar_arrive_expect_tx(bX, nh * S::kTile);
                         for (int i = 0; i < nh; ++i) tma_load_3d(sm + S::kX + i * S::kTile, &tm.x, 0, h0 + i, t0, bX);
@@ -710,12 +720,14 @@ __global__ void __launch_bounds__(kVarThreads, 1)
         }
         hand_on(false, 0, 0, 0, 0, nullptr, nullptr, nullptr, nullptr);  // (after a failure too, for those who can still hear it)
         __syncwarp();
-    } else if (warp == kTableWarp) {
-        // ---- the tables: running sums and factors.  Half a warp per head, eight rows per
-        // lane; the next chunk's dt is on its way while this one's are formed. --------------
-        const int hh = lane >> 4, sub = lane & 15;
+    } else if (warp >= kTableWarp && warp < kTableWarp + kTables) {
+        // ---- the tables: running sums and factors.  Half a warp per head, eight rows per lane
+        // (a warp and four where there are two); the next chunk's dt is on its way while this
+        // one's are formed. ----------------------------------------------------------------
+        constexpr int kLanes = 16 * kTables, kRows = kVarQ / kLanes;
+        const int hh = SUMMARY ? warp - kTableWarp : lane >> 4, sub = lane & (kLanes - 1);
         uint32_t u = 0, k = 0;  // chunks handed on, items taken
-        // the item at hand, with this half's A, bias and D
+        // the item at hand, with this head's A, bias and D
         int first_t = 0, stop_t = 0, h0 = 0, nh = 0, g = 0;
         const float *src = nullptr;
         float *dst = nullptr, *decay = nullptr;
@@ -733,80 +745,87 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             ++k;
             return valid;
         };
-        uint16_t raw[8];
+        uint16_t raw[kRows];
         auto load_dt = [&](int64_t t) {
             const uint16_t *from = static_cast<const uint16_t *>(p.dt) + h0 + hh;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t r = t + 8 * sub + i;
+            for (int i = 0; i < kRows; ++i) {
+                const int64_t r = t + kRows * sub + i;
                 raw[i] = r < stop_t && hh < nh ? __ldg(from + r * p.dt_stride) : static_cast<uint16_t>(0);
             }
         };
         auto ready = [&]() -> bool { return u == 0 || wait(bEmpty, (u - 1) & 1u); };  // everyone has read the chunk before
+        // The first of the two passes walks an item from its last chunk to its first, the sum of
+        // the later chunks' dt A in the columns' factors: its state only collects products.
+        auto begin = [&]() -> int { return SUMMARY ? first_t + (stop_t - first_t - 1) / kVarQ * kVarQ : first_t; };
         bool ok = true, more = take();
-        int t = first_t;
+        int t = begin();
         if (more) load_dt(t);
-        float item_total = 0.0f;
+        float item_total = 0.0f;  // of the item's chunks so far
         while (more) {
-            const int rows = min(kVarQ, stop_t - t);
-            const bool first = t == first_t, last = t + rows >= stop_t, mine = hh < nh;
-            float dt[8], d[8];
+            const int rows = min(kVarQ, stop_t - t), next = SUMMARY ? t - kVarQ : t + kVarQ;
+            const bool low = t == first_t, high = t + rows >= stop_t, mine = hh < nh;
+            const bool first = SUMMARY ? high : low, last = SUMMARY ? low : high;
+            float dt[kRows], d[kRows];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kRows; ++i) {
                 dt[i] = __uint_as_float(static_cast<uint32_t>(raw[i]) << 16) + bias;
                 if (p.softplus) dt[i] = softplus_accurate(dt[i]);
-                if (8 * sub + i >= rows || !mine) dt[i] = 0.0f;
+                if (kRows * sub + i >= rows || !mine) dt[i] = 0.0f;
             }
-            if (!last) load_dt(t + rows);
+            if (!last) load_dt(next);
             // d_j = minus the sum of the later rows' dt A
             float after = 0.0f;
 #pragma unroll
-            for (int i = 7; i >= 0; --i) {
+            for (int i = kRows - 1; i >= 0; --i) {
                 d[i] = after;
                 after -= dt[i] * A;
             }
             float sum = after;
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) {
-                const float v = __shfl_down_sync(0xffffffffu, sum, o, 16);
-                if (sub + o < 16) sum += v;
+            for (int o = 1; o < kLanes; o <<= 1) {
+                const float v = __shfl_down_sync(0xffffffffu, sum, o, kLanes);
+                if (sub + o < kLanes) sum += v;
             }
-            const float T = -__shfl_sync(0xffffffffu, sum, 0, 16);
-            float later = __shfl_down_sync(0xffffffffu, sum, 1, 16);
-            if (sub == 15) later = 0.0f;
-            float most = fabsf(T), w[8], span = 0.0f;
+            const float T = -__shfl_sync(0xffffffffu, sum, 0, kLanes);
+            float later = __shfl_down_sync(0xffffffffu, sum, 1, kLanes);
+            if (sub == kLanes - 1) later = 0.0f;
+            float most = fabsf(T), w[kRows], span = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kRows; ++i) {
                 d[i] += later;
                 most = fmaxf(most, fabsf(d[i]));
             }
-            const float block = __shfl_sync(0xffffffffu, d[0], lane & ~1);  // d of the first of these 16 rows
+            const float block = __shfl_sync(0xffffffffu, d[0], lane & ~(16 / kRows - 1));  // d of the first of these 16 rows
 #pragma unroll
-            for (int i = 0; i < 8; ++i) span = fmaxf(span, fabsf(block - d[i]));
+            for (int i = 0; i < kRows; ++i) span = fmaxf(span, fabsf(block - d[i]));
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) {
+            for (int o = kLanes / 2; o > 0; o >>= 1) {
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
                 span = fmaxf(span, __shfl_xor_sync(0xffffffffu, span, o));
             }
-            const VarDecays decays = most <= kVarRange ? kVarByColumn : span <= kVarSpan ? kVarByBlock : kVarOneByOne;
-            const float from = decays == kVarByColumn ? 0.0f : block;
+            if (first) item_total = 0.0f;
+            const VarDecays decays = SUMMARY || most <= kVarRange ? kVarByColumn : span <= kVarSpan ? kVarByBlock : kVarOneByOne;
+            const float from = SUMMARY ? item_total : decays == kVarByColumn ? 0.0f : block;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = decays == kVarOneByOne ? dt[i] : expf(from - d[i]) * dt[i];
-            item_total = (first ? 0.0f : item_total) + T;
+            for (int i = 0; i < kRows; ++i) w[i] = decays == kVarOneByOne ? dt[i] : expf(from - d[i]) * dt[i];
+            item_total += T;
             if (!ready()) {
                 ok = false;
                 break;
             }
-            float4 *pd = reinterpret_cast<float4 *>(tabD + hh * kVarQ + 8 * sub), *pw = reinterpret_cast<float4 *>(tabW + hh * kVarQ + 8 * sub);
-            pd[0] = make_float4(d[0], d[1], d[2], d[3]), pd[1] = make_float4(d[4], d[5], d[6], d[7]);
-            pw[0] = make_float4(w[0], w[1], w[2], w[3]), pw[1] = make_float4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+            for (int i = 0; i < kRows; i += 4) {
+                *reinterpret_cast<float4 *>(tabD + hh * kVarQ + kRows * sub + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+                *reinterpret_cast<float4 *>(tabW + hh * kVarQ + kRows * sub + i) = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+            }
             VarChunk *out = info + (u & 1u);
             if (sub == 0) {
                 out->decay[hh] = expf(T), out->scale[hh] = decays == kVarByColumn ? expf(T) : 1.0f, out->D[hh] = D;
                 out->ref[hh] = T, out->decays[hh] = decays;
                 if (SUMMARY && last && mine) decay[hh] = expf(item_total);
             }
-            if (lane == 0) {
+            if (lane == 0 && (!SUMMARY || hh == 0)) {
                 out->t0 = t, out->rows = rows;
                 out->h0 = h0, out->nh = nh, out->g = g;
                 out->first = first, out->last = last, out->stop = 0;
@@ -815,15 +834,15 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             __syncwarp();
             if (lane == 0) ssd_arrive(bFull);
             ++u;
-            t += rows;
+            t = next;
             if (last) {
                 more = take();
-                t = first_t;
+                t = begin();
                 if (more) load_dt(t);
             }
         }
         if (ok && ready() && lane == 0) {
-            info[u & 1u].stop = 1;
+            if (!SUMMARY || hh == 0) info[u & 1u].stop = 1;
             ssd_arrive(bFull);
         }
         __syncwarp();
@@ -898,6 +917,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
             };
 #pragma unroll 1
             for (int q0 = c0; q0 < c0 + kCols; q0 += 32) {
+                if (SUMMARY && !first) break;  // no decay between its chunks
                 float v[16], v2[16];
                 if (!first) {
                     ssd_ld16x2(tSh + q0, v, tSh + q0 + 16, v2);
