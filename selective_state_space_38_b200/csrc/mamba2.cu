@@ -499,8 +499,8 @@ int64_t var_pairs(const ssm_ssd_packed_dims_t *d) {
 
 // Tokens of a segment of the two passes: two to seven chunks, about three segments to each of 148
 // SMs (a segment costs about half a chunk more for its state, and the last ones should even out;
-// one sequence of 32768 with 24 heads: 219 us with seven chunks, 250 with four; 20 ragged ones: 85
-// with two, 118 with five, before the last changes to the kernel); longer where a thousand segments or sixteen to each SM would not do,
+// one sequence of 32768 with 24 heads: 193 us with seven chunks, 229 with five; 20 ragged ones: 82
+// with two, 88 with three); longer where a thousand segments or sixteen to each SM would not do,
 // which bounds the states in the workspace.
 int64_t var_segment(const ssm_ssd_packed_dims_t *d) {
     const int64_t chunks = (d->tokens + kVarQ - 1) / kVarQ;

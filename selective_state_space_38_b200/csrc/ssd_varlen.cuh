@@ -31,7 +31,7 @@
 // most for the state have the smallest rounding.
 //
 // Per pair of heads and chunk: 96 KB loaded through TMA and six products of
-// 128 x 128 x 128, 3072 cycles of the tensor pipe at 8192 bf16 flops a cycle;
+// 128 x 128 x 128, 512 cycles of the tensor pipe each at 8192 bf16 flops a cycle;
 // shared memory carries about 640 KB for them and their operands, 5000 cycles at
 // 128 bytes a cycle, and bounds it together with the chain from a chunk's state to the
 // next one's (about 8600 cycles are measured).  4 x 4096 tokens of 80 heads in one
