@@ -512,7 +512,8 @@ int64_t var_segment(const ssm_ssd_packed_dims_t *d) {
 }
 
 // Workspace: [0, 256) header, the units, the later segments, the flags, the decays, then (256-byte
-// aligned) the states that pass between segments or CTAs.
+// aligned) the states that pass between segments or CTAs, and the starting states of the sequences
+// of several segments (each has a window in which its second one starts, so they are no more than those).
 size_t var_layout(const ssm_ssd_packed_dims_t *d, uint8_t *base, VarWork *w) {
     const int64_t windows = (d->tokens + var_segment(d) - 1) / var_segment(d);
     size_t at = 256;
@@ -526,6 +527,8 @@ size_t var_layout(const ssm_ssd_packed_dims_t *d, uint8_t *base, VarWork *w) {
     at += static_cast<size_t>(windows) * d->heads * 4;
     const size_t carry = at = (at + 255) / 256 * 256;
     at += std::max<size_t>(static_cast<size_t>(windows > 1 ? windows : 0) * d->heads, kVarMaxCtas * kVarHeads) * kSsdP * kSsdN * 4;
+    const size_t start = at;
+    at += static_cast<size_t>(windows > 1 ? std::min(d->sequences, windows) : 0) * d->heads * kSsdP * kSsdN * 4;
     if (w) {
         w->queue = reinterpret_cast<uint32_t *>(base);
         w->error = reinterpret_cast<uint32_t *>(base + 16);
@@ -538,6 +541,7 @@ size_t var_layout(const ssm_ssd_packed_dims_t *d, uint8_t *base, VarWork *w) {
         w->flags = reinterpret_cast<uint32_t *>(base + flags);
         w->decay = reinterpret_cast<float *>(base + decay);
         w->carry = reinterpret_cast<float *>(base + carry);
+        w->start = reinterpret_cast<float *>(base + start);
     }
     return at;
 }

@@ -54,7 +54,10 @@
 // first, when some are longer than that.  And two passes over segments of the
 // sequences when the longest chain would leave the other SMs idle: the segments' own
 // states first, from zeros and without outputs, all at once, then the states at their
-// starts (ssd_varlen_combine_kernel), then every segment by itself.
+// starts (ssd_varlen_combine_kernel), then every segment by itself.  In that last pass
+// the segments of a sequence run in any order on any CTAs, and the one that ends it
+// writes its cache row: so none of them reads that row.  The first one starts from a
+// copy that the joining kernel, which reads the row anyhow, leaves in the workspace.
 #pragma once
 
 #include <cuda.h>
@@ -80,8 +83,9 @@ constexpr int kVarParts = 3;        // bf16 parts of w x
 // Workspace: header (error word at 16, where ssm_scan_fwd_status reads it); the units
 // (chunks x pairs) before each sequence; for the two passes the later segments of the
 // sequences and, by the window of `segment` tokens each starts in, a decay and a state
-// per head; for the ranges a flag and a pair of states per CTA (the states of both
-// share one place).
+// per head, and the starting states of the sequences of several segments, by their
+// number among those; for the ranges a flag and a pair of states per CTA (the carried
+// states of both share one place).
 struct VarWork {
     uint32_t *queue;                   // item counters of the two passes; order of the CTAs' start
     uint32_t *error, *extras;          // error word; later segments
@@ -92,6 +96,7 @@ struct VarWork {
     uint32_t *flags;                   // [kVarMaxCtas] a range's head is handed on
     float *decay;                      // [windows][heads] of the segment before the window's
     float *carry;                      // [windows][heads][P][N], or [kVarMaxCtas][2][P][N]
+    float *start;                      // [sequences of several segments][heads][P][N]
 };
 
 enum VarMode : uint32_t { kVarRanges = 0, kVarTwoPasses = 1, kVarChains = 2 };
@@ -245,7 +250,7 @@ __global__ void __launch_bounds__(1024) ssd_varlen_setup_kernel(const VarParams 
 }
 
 // The states at the segments' starts from the segments' own: S_{s+1} = exp(T_s) S_s
-// + E_s, in place.  grid: (heads x 8, sequences of more than one segment at most)
+// + E_s, in place, and a copy of S_0 from the cache where a sequence goes on.  grid: (heads x 8, sequences of more than one segment at most)
 __global__ void __launch_bounds__(256) ssd_varlen_combine_kernel(const VarParams p) {
     release_next();
     wait_previous();
@@ -258,8 +263,10 @@ __global__ void __launch_bounds__(256) ssd_varlen_combine_kernel(const VarParams
         const int segs = static_cast<int>((end - begin + p.segment - 1) / p.segment);
         const int slot = p.states ? packed_slot(p.seq, n) : -1;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (slot >= 0 && p.seq.has_initial && p.seq.has_initial[n])
+        if (slot >= 0 && p.seq.has_initial && p.seq.has_initial[n]) {
             s = reinterpret_cast<const float4 *>(p.states + (static_cast<int64_t>(slot) * p.heads + h) * (kSsdP * kSsdN))[e];
+            reinterpret_cast<float4 *>(p.work.start + (static_cast<int64_t>(i) * p.heads + h) * (kSsdP * kSsdN))[e] = s;
+        }
         for (int k0 = 1; k0 < segs; k0 += 8) {  // eight segments' loads at a time
             float4 v[8];
             float a[8];
@@ -624,6 +631,13 @@ __global__ void __launch_bounds__(SUMMARY ? kVarSummaryThreads : kVarThreads, 1)
             *initial = s && p.seq.has_initial && p.seq.has_initial[n] ? s : nullptr;
             return s;
         };
+        // the sequences of several segments before n (their second segments lead the list, in packed order)
+        auto several_before = [&](int n) -> int {
+            const int several = static_cast<int>(*reinterpret_cast<volatile uint32_t *>(p.work.several));
+            int c = 0;
+            for (int i = lane; i < several; i += 32) c += p.work.list[i].x < n;
+            return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(c)));
+        };
         bool ok = true;
         if (mode != kVarRanges) {
             // segments: every sequence's first, then the later ones of the list; chains: the
@@ -658,6 +672,7 @@ __global__ void __launch_bounds__(SUMMARY ? kVarSummaryThreads : kVarThreads, 1)
                     const float *src;
                     float *state = cache(n, pair, &src);
                     if (seg > 0) src = p.work.carry + (window * p.heads + h0) * (kSsdP * kSsdN);
+                    else if (src && stop < end) src = p.work.start + (static_cast<int64_t>(several_before(n)) * p.heads + h0) * (kSsdP * kSsdN);
                     ok = hand_on(true, n, pair, first, stop, src, stop < end ? nullptr : state, nullptr, nullptr);
                 }
             }
