@@ -437,6 +437,8 @@ __global__ void __launch_bounds__(kConvThreads, 8) conv1d_bwd_kernel(const Conv1
 
 // dst[c * stride_c + k] = sum over tiles of partial[tile][k][c], tiles in order
 // within each of the 8 rows of a block and the rows in order.  grid: (dim / 32, K + 1)
+// (`partial` is loaded from L2: its blocks come while the kernel before still writes it,
+// so the read-only path, which may keep what it held before the wait, is not for it)
 __global__ void __launch_bounds__(256) conv1d_reduce_kernel(const float *partial, float *dw, float *dbias, int64_t dim,
                                                             int64_t tiles, int K) {
     __shared__ float part[8][32];
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(256) conv1d_reduce_kernel(const float *partial
     float s = 0.0f;
     if (c < dim) {
 #pragma unroll 8
-        for (int64_t t = threadIdx.y; t < tiles; t += 8) s += __ldg(partial + (t * (K + 1) + k) * dim + c);
+        for (int64_t t = threadIdx.y; t < tiles; t += 8) s += __ldcg(partial + (t * (K + 1) + k) * dim + c);
     }
     part[threadIdx.y][threadIdx.x] = s;
     __syncthreads();

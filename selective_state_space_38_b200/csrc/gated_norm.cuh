@@ -301,6 +301,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) gated_norm_bwd_kernel(const N
 }
 
 // dweight[c] = sum over the slots of partial[slot][c], in a fixed order.  grid: dim / 32
+// (`partial` is loaded from L2: its blocks come while the kernel before still writes it,
+// so the read-only path, which may keep what it held before the wait, is not for it)
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *partial, float *dweight, int64_t dim, int64_t slots) {
     __shared__ float part[32][33];
     wait_previous();
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *partial,
     float s = 0.0f;
     if (c < dim) {
 #pragma unroll 4
-        for (int64_t t = threadIdx.y; t < slots; t += 32) s += __ldg(partial + t * dim + c);
+        for (int64_t t = threadIdx.y; t < slots; t += 32) s += __ldcg(partial + t * dim + c);
     }
     part[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
