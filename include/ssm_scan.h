@@ -347,8 +347,10 @@ int ssm_ssd_fwd(const void *x, const void *dt, const float *dt_bias, int softplu
  * cu_seqlens[i] .. cu_seqlens[i + 1] - 1.
  *
  *   cu_seqlens     [sequences + 1] int32 on the device, ascending, within
- *                  [0, tokens]; a sequence may be empty.  Rows behind the last
- *                  sequence are left as they were in every output.
+ *                  [0, tokens]; a sequence may be empty, and the first may start
+ *                  behind row 0.  Rows before the first sequence and behind the
+ *                  last are left as they were in every output, and what they hold
+ *                  reaches nothing.
  *   slots          optional [sequences] int32 on the device: the row of the cache
  *                  (windows, states) that belongs to each sequence (NULL: sequence
  *                  i's is i).  A slot outside [0, slots) stands for none: the
@@ -434,8 +436,8 @@ int ssm_conv1d_step(void *windows, const int32_t *slots, const void *x, const fl
 /*
  * Gradients of ssm_conv1d_fwd on sequences that start from zeros, given dy:
  * dx in the activation dtype, dw [dim][K] and dbias (optional, [dim]) float32,
- * summed in a fixed order (equal calls give equal bits).  Rows of dx behind the
- * last sequence are left as they were.  workspace: at least
+ * summed in a fixed order (equal calls give equal bits).  Rows of dx outside the
+ * sequences are left as they were.  workspace: at least
  * ssm_conv1d_bwd_workspace_size bytes, 16-byte aligned.
  */
 int ssm_conv1d_bwd_workspace_size(const ssm_conv1d_dims_t *dims, size_t *bytes);

@@ -50,7 +50,8 @@ constexpr int kConvBwdBatch = 4;
 // The sequences of a block's tile, rows counted from the tile's first (32 bits).  All
 // rows are walked by every thread of the block in step, so the current sequence is
 // the block's; the first 32 from the tile's start wait in shared memory, since each
-// would cost dependent loads.
+// would cost dependent loads.  Rows before the first sequence's start are in none; behind
+// it a sequence starts where the one before ends.
 struct ConvWalk {
     int n;           // the current sequence (`sequences`: none any more)
     int start, end;  // its rows
@@ -184,8 +185,14 @@ __global__ void __launch_bounds__(kConvThreads, 12) conv1d_fwd_kernel(const Conv
     };
     load(0);
     q.enter(p);
+    int first = 0;
+    if (q.start > 0) {  // rows before the first sequence stay as they were
+        first = min(q.start, rows);
+        x += (first - kConvBatch) * xs, y += first * ys;
+        load(first);
+    }
     ch.taps(p, c);
-    ch.history(p, q, 0, c);
+    ch.history(p, q, first, c);
     auto row = [&](const typename R::Raw &r) {  // `y` is its row
         Lanes<kL> v[kN], u[kN];
 #pragma unroll
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(kConvThreads, 12) conv1d_fwd_kernel(const Conv
         R::store(y, 0, u);
         y += ys;
     };
-    for (int r = 0; r < rows; r += kConvBatch) {
+    for (int r = first; r < rows; r += kConvBatch) {
         typename R::Raw now[kConvBatch];
 #pragma unroll
         for (int i = 0; i < kConvBatch; ++i) now[i] = raw[i];
@@ -399,7 +406,7 @@ __global__ void __launch_bounds__(kConvThreads, 8) conv1d_bwd_kernel(const Conv1
             const int s = r + e;
             if (s >= last) break;
             if (q.n < p.seq.sequences && s >= q.end && q.to(p, s)) ch.history(p, q, s, c);
-            const bool live = q.n < p.seq.sequences && s < have;
+            const bool live = q.n < p.seq.sequences && s >= q.start && s < have;
 #pragma unroll
             for (int d = K - 1; d > 0; --d) eh[d] = eh[d - 1];
             eh[0] = live ? q.end : -1;

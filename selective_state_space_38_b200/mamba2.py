@@ -171,7 +171,7 @@ def ssm_conv1d_fwd(x, conv_w, conv_bias, cu_seqlens, windows=None, slots=None, h
     [slots, K-1, dim] (x's dtype) holds inputs before a sequence, oldest first:
     read for the sequences that ``has_initial`` [n] (bool) marks, and left holding
     every sequence's last K-1 inputs; ``slots`` [n] int32 names the rows.  Returns
-    out [tokens, dim]; rows behind the last sequence are not written."""
+    out [tokens, dim]; rows outside the sequences are not written."""
     dev = _cuda(x, 2, "x")
     T, dim = x.shape
     act, f32 = x.dtype, torch.float32
@@ -221,7 +221,7 @@ def ssm_conv1d_step(windows, x, conv_w, conv_bias, slots=None, silu=True, out=No
 
 def ssm_conv1d_bwd(x, conv_w, conv_bias, cu_seqlens, dy, silu=True, dx=None, stream=None, workspace=None):
     """Gradients of ssm_conv1d_fwd on sequences that start from zeros.  Returns a
-    dict: dx [tokens, dim] in x's dtype (rows behind the last sequence are not
+    dict: dx [tokens, dim] in x's dtype (rows outside the sequences are not
     written), dw [dim, K] and dbias [dim] (None without conv_bias) float32."""
     dev = _cuda(x, 2, "x")
     T, dim = x.shape
@@ -274,7 +274,7 @@ def ssm_ssd_varlen_fwd(x, dt, dt_bias, softplus, A, B, C, D, cu_seqlens, states=
     ``states`` [slots, heads, 64, 128] float32 is read for the sequences that
     ``has_initial`` [n] (bool) marks and left holding every sequence's state;
     ``slots`` [n] int32 names the rows.  Returns out [tokens, heads, 64]; rows
-    behind the last sequence are not written.  ``check=True`` waits for the call
+    outside the sequences are not written.  ``check=True`` waits for the call
     and raises SSMError when cu_seqlens did not ascend within the tokens or a
     bounded device wait gave up."""
     dev = _cuda(x, 3, "x")
