@@ -468,6 +468,12 @@ int ssm_conv1d_bwd(const void *x, const float *w, const float *bias, const int32
  * where few sequences leave SMs idle they are cut into segments whose own states are
  * formed first and joined afterwards, which may change the last bits of a state.
  * Equal calls on one GPU model give equal bits.
+ * Rounding: the states are sums in float32 (the products' operands have 24 bits).  y's
+ * two products take bf16 operands, C B^T with the decays and the state before the chunk
+ * each rounded once, as y itself is; ssm_ssd_fwd takes two bf16 parts of each there.
+ * These operands keep their precision for values of x, B, C B^T and the states between
+ * some 2^-75 and 2^76, whatever the decays (of steps dt of one sign): smaller ones count
+ * by that much absolutely.
  */
 int ssm_ssd_varlen_fwd_workspace_size(const ssm_ssd_packed_dims_t *dims, size_t *bytes);
 int ssm_ssd_varlen_fwd(const void *x, const void *dt, const float *dt_bias, int softplus, const float *A,

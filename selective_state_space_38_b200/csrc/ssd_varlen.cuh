@@ -15,14 +15,19 @@
 // it meets x itself, and the row factor exp(d_i) waits for the end.  (Scaling x by w
 // instead would save the per-head matrix, but the tensor core aligns a sum's products
 // to the largest and counts a masked zero as 2^-126 times its x: with x scaled over
-// e^110 the first rows of a chunk came out wrong by their whole value.)  Where |d|
-// passes kVarRange the factors would leave bfloat16's range: there the matrix takes
-// its decays against a row factor exp(cs_i), held to e^-70 at least, and S comes
+// e^110 the first rows of a chunk came out wrong by their whole value.)  Where the
+// decays span more than e^kVarRange the factors would leave bfloat16's range: there the
+// matrix takes its decays against a row factor exp(cs_i), held to e^-70 at least, and S comes
 // unscaled.  Its decays are then, for a block of 16 columns from j0 on, one factor of
 // the row, exp(c_i - d_j0), times w_j = exp(d_j0 - d_j) dt_j, or, where d moves by more
 // than kVarSpan within 16 steps, formed one by one.  (One by one throughout, the heads
 // of such decays took 1.25 times the others' time, and at 4 x 4096 their CTAs 220 us
 // where the median took 180.)  The state accumulates in tensor memory on exp(T) S.
+// The matrix and S also take a power of two, 2^k, and the row's factor 2^-k, with k
+// from the middle of the decays' exponents: the factors then span e^-35 to e^35 instead
+// of e^-70 to 1 or 1 to e^70, so that neither small operands fall below bfloat16's
+// normal values (without it a state of 1e-11 vanished at T = -69) nor large ones pass
+// float32's (C B^T dt x of 1e8 at T = -71).
 //
 // Roundings to bf16 are those of the tensor core's operands: C B^T with its factors
 // once, S once where it meets C (each at most the half step that y's own rounding
@@ -70,7 +75,8 @@ namespace ssm {
 constexpr int kVarQ = 128;          // steps of a chunk at most
 constexpr int kVarMaxWindows = 1024;
 constexpr int kVarMaxCtas = 160;
-constexpr float kVarRange = 70.0f;
+constexpr float kVarRange = 70.0f;   // of the exponents of the factors by columns, and of the rows' on the side of decay
+constexpr float kVarGrowth = 85.0f;  // rows' exponents on the side of growth
 constexpr float kVarSpan = 40.0f;  // e^40 and e^-87 keep the products of a block's factors well inside float32
 constexpr int kVarHalf = 256;       // epilogue threads on the state, and on the output
 // + a warp for the MMAs, the tables, the loads and the work list each; the first of the two passes has
@@ -146,6 +152,7 @@ struct VarChunk {
     uint32_t *flag;
     float decay[2], scale[2], D[2];  // exp(T); of S where it meets C
     float ref[2];            // T: cs = d + T, the row factor's exponent where the decays are not by columns
+    float down[2], shift[2]; // 2^-k and its exponent k ln 2, where C B^T with its factors and S take 2^k
     int32_t decays[2];       // VarDecays
 };
 
@@ -317,9 +324,10 @@ struct VarRange {
 
 // The exponent of a row's factor.  Where the decays are not taken by columns it is cs_i,
 // held to [-70, 85] (beyond, only the state before the chunk would feel it, by e^-70
-// of itself; growth by e^85 overflows), and the rest is left to the matrix.
+// of itself; growth by e^85 overflows), and the rest is left to the matrix.  2^k comes
+// off here (its rounded exponent changes y by 2^-18 of itself at most).
 __device__ __forceinline__ float var_row_exponent(const VarChunk &c, int i, float di) {
-    return c.decays[i] == kVarByColumn ? di : fminf(fmaxf(di + c.ref[i], -kVarRange), 85.0f);
+    return (c.decays[i] == kVarByColumn ? di : fminf(fmaxf(di + c.ref[i], -kVarRange), kVarGrowth)) - c.shift[i];
 }
 
 // C B^T with the factors of both heads, as bf16, over its own columns: of this warp's
@@ -805,11 +813,12 @@ __global__ void __launch_bounds__(SUMMARY ? kVarSummaryThreads : kVarThreads, 1)
             const float T = -__shfl_sync(0xffffffffu, sum, 0, kLanes);
             float later = __shfl_down_sync(0xffffffffu, sum, 1, kLanes);
             if (sub == kLanes - 1) later = 0.0f;
-            float most = fabsf(T), w[kRows], span = 0.0f;
+            const float half = 0.5f * T;  // d lies between 0 and -T where dt has one sign
+            float most = fabsf(half), w[kRows], span = 0.0f;
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
                 d[i] += later;
-                most = fmaxf(most, fabsf(d[i]));
+                most = fmaxf(most, fabsf(d[i] + half));
             }
             const float block = __shfl_sync(0xffffffffu, d[0], lane & ~(16 / kRows - 1));  // d of the first of these 16 rows
 #pragma unroll
@@ -820,10 +829,16 @@ __global__ void __launch_bounds__(SUMMARY ? kVarSummaryThreads : kVarThreads, 1)
                 span = fmaxf(span, __shfl_xor_sync(0xffffffffu, span, o));
             }
             if (first) item_total = 0.0f;
-            const VarDecays decays = SUMMARY || most <= kVarRange ? kVarByColumn : span <= kVarSpan ? kVarByBlock : kVarOneByOne;
-            const float from = SUMMARY ? item_total : decays == kVarByColumn ? 0.0f : block;
+            const bool wide = !SUMMARY && most > 0.5f * kVarRange;
+            const VarDecays decays = !wide ? kVarByColumn : span <= kVarSpan ? kVarByBlock : kVarOneByOne;
+            // the middle of the exponents of the columns' factors, or of the rows', which are those of cs; these
+            // go from 0 to T, or where dt changes its sign somewhere on both sides
+            const float centre = SUMMARY ? 0.0f : !wide ? -half : most > fabsf(half) + 1.0f ? 0.0f : 0.5f * fminf(fmaxf(T, -kVarRange), kVarGrowth);
+            const int k2 = __float2int_rn(centre * kLog2e);  // |k2| < 127
+            const float up = __int_as_float((127 + k2) << 23);
+            const float from = SUMMARY ? item_total : decays == kVarByColumn ? 0.0f : block, by = decays == kVarByColumn ? up : 1.0f;
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) w[i] = decays == kVarOneByOne ? dt[i] : expf(from - d[i]) * dt[i];
+            for (int i = 0; i < kRows; ++i) w[i] = decays == kVarOneByOne ? dt[i] : expf(from - d[i]) * by * dt[i];
             item_total += T;
             if (!ready()) {
                 ok = false;
@@ -836,8 +851,9 @@ __global__ void __launch_bounds__(SUMMARY ? kVarSummaryThreads : kVarThreads, 1)
             }
             VarChunk *out = info + (u & 1u);
             if (sub == 0) {
-                out->decay[hh] = expf(T), out->scale[hh] = decays == kVarByColumn ? expf(T) : 1.0f, out->D[hh] = D;
+                out->decay[hh] = expf(T), out->scale[hh] = decays == kVarByColumn ? expf(T) * up : up, out->D[hh] = D;
                 out->ref[hh] = T, out->decays[hh] = decays;
+                out->down[hh] = __int_as_float((127 - k2) << 23), out->shift[hh] = static_cast<float>(k2) * kLn2;
                 if (SUMMARY && last && mine) decay[hh] = expf(item_total);
             }
             if (lane == 0 && (!SUMMARY || hh == 0)) {
@@ -908,6 +924,9 @@ __global__ void __launch_bounds__(SUMMARY ? kVarSummaryThreads : kVarThreads, 1)
             const L2 decay = lanes<2>(c.decay[head]);
             const float scale = c.scale[head];
             float w = tabW[head * kVarQ + row];
+            if constexpr (!SUMMARY) {
+                if (c.decays[head] == kVarByColumn) w *= c.down[head];
+            }
             if (c.decays[head] != kVarByColumn)  // what is missing of exp(-d) dt
                 w *= expf(-tabD[head * kVarQ + (c.decays[head] == kVarByBlock ? row & ~15 : row)]);
             if constexpr (SUMMARY) ssd_arrive(bEmpty);
