@@ -71,16 +71,23 @@ int conv_setup(const void *x, const float *w, const float *bias, const ssm_conv1
     if (!d || !x || !w) return SSM_ERR_INVALID_ARG;
     if (d->tokens < 1 || d->dim < 1 || d->slots < 0) return SSM_ERR_INVALID_ARG;
     if (d->width < 1 || d->width > 4 || !dtype_ok(d->act_dtype)) return SSM_ERR_UNSUPPORTED;
-    if (d->tokens > INT32_MAX || d->sequences > INT32_MAX || d->slots > INT32_MAX || d->dim > INT32_MAX)
-        return SSM_ERR_UNSUPPORTED;
+    if (d->tokens > INT32_MAX || d->slots > INT32_MAX || d->dim > INT32_MAX) return SSM_ERR_UNSUPPORTED;
     if (d->x_stride < d->dim || !rows_ok(d->tokens, d->x_stride)) return SSM_ERR_INVALID_ARG;
     const size_t es = d->act_dtype == SSM_F32 ? 4 : 2;
     if (!aligned_to(x, es) || !aligned4(w) || !aligned4(bias)) return SSM_ERR_MISALIGNED;
     memset(p, 0, sizeof *p);
     p->x = x, p->w = w, p->bias = bias;
     p->dim = d->dim, p->x_stride = d->x_stride, p->silu = d->silu ? 1 : 0;
-    p->seq.tokens = d->tokens;
-    p->seq.sequences = static_cast<int32_t>(d->sequences), p->seq.nslots = static_cast<int32_t>(d->slots);
+    p->seq.tokens = d->tokens, p->seq.nslots = static_cast<int32_t>(d->slots);
+    return SSM_OK;
+}
+
+// The packed sequences of the forward pass and of the gradients (the step has none).
+int conv_sequences(const int32_t *cu_seqlens, const ssm_conv1d_dims_t *d, Conv1dParams *p) {
+    if (!cu_seqlens || d->sequences < 1) return SSM_ERR_INVALID_ARG;
+    if (d->sequences > INT32_MAX) return SSM_ERR_UNSUPPORTED;
+    if (!aligned4(cu_seqlens)) return SSM_ERR_MISALIGNED;
+    p->seq.cu = cu_seqlens, p->seq.sequences = static_cast<int32_t>(d->sequences);
     return SSM_OK;
 }
 
@@ -156,12 +163,13 @@ int ssm_conv1d_fwd(const void *x, const float *w, const float *bias, const int32
                    const int32_t *slots, const uint8_t *has_initial, void *y, const ssm_conv1d_dims_t *dims,
                    ssm_stream_t stream) {
     Conv1dParams p;
-    const int rc = conv_setup(x, w, bias, dims, &p);
+    int rc = conv_setup(x, w, bias, dims, &p);
+    if (rc == SSM_OK) rc = conv_sequences(cu_seqlens, dims, &p);
     if (rc != SSM_OK) return rc;
-    if (!cu_seqlens || !y || dims->sequences < 1) return SSM_ERR_INVALID_ARG;
+    if (!y) return SSM_ERR_INVALID_ARG;
     if (dims->y_stride < dims->dim || !rows_ok(dims->tokens, dims->y_stride)) return SSM_ERR_INVALID_ARG;
     const int64_t es = dims->act_dtype == SSM_F32 ? 4 : 2, K = dims->width;
-    if (!aligned_to(y, es) || !aligned_to(windows, es) || !aligned4(cu_seqlens) || !aligned4(slots)) return SSM_ERR_MISALIGNED;
+    if (!aligned_to(y, es) || !aligned_to(windows, es) || !aligned4(slots)) return SSM_ERR_MISALIGNED;
     if (!rows_ok(dims->slots, (K - 1) * dims->dim)) return SSM_ERR_INVALID_ARG;
     const int64_t cache = windows ? dims->slots * (K - 1) * dims->dim * es : 0;
     const Rows ins[] = {{x, dims->tokens, dims->dim * es, dims->x_stride * es}, flat(w, dims->dim * K * 4),
@@ -170,7 +178,7 @@ int ssm_conv1d_fwd(const void *x, const float *w, const float *bias, const int32
     const Rows outs[] = {{y, dims->tokens, dims->dim * es, dims->y_stride * es}, flat(windows, cache)};
     if (outputs_clash(ins, outs)) return SSM_ERR_INVALID_ARG;
     p.windows = windows, p.y = y, p.y_stride = dims->y_stride;
-    p.seq.cu = cu_seqlens, p.seq.slots = slots, p.seq.has_initial = has_initial;
+    p.seq.slots = slots, p.seq.has_initial = has_initial;
     const bool vec = vector_rows({x, y, windows, w, bias}, {dims->x_stride, dims->y_stride}, dims->dim, dims->act_dtype);
     p.tile = conv_tile(dims->tokens, dims->dim, 64);
     const int64_t tiles = (dims->tokens + p.tile - 1) / p.tile;
@@ -231,16 +239,16 @@ int ssm_conv1d_bwd(const void *x, const float *w, const float *bias, const int32
                    float *dw, float *dbias, void *workspace, size_t workspace_bytes, const ssm_conv1d_dims_t *dims,
                    ssm_stream_t stream) {
     Conv1dParams p;
-    const int rc = conv_setup(x, w, bias, dims, &p);
+    int rc = conv_setup(x, w, bias, dims, &p);
+    if (rc == SSM_OK) rc = conv_sequences(cu_seqlens, dims, &p);
     if (rc != SSM_OK) return rc;
-    if (!cu_seqlens || !dy || !dx || !dw || !workspace || dims->sequences < 1) return SSM_ERR_INVALID_ARG;
+    if (!dy || !dx || !dw || !workspace) return SSM_ERR_INVALID_ARG;
     if (dims->dy_stride < dims->dim || dims->dx_stride < dims->dim || !rows_ok(dims->tokens, dims->dy_stride) ||
         !rows_ok(dims->tokens, dims->dx_stride))
         return SSM_ERR_INVALID_ARG;
     if (workspace_bytes < conv_bwd_bytes(dims)) return SSM_ERR_INVALID_ARG;
     const int64_t es = dims->act_dtype == SSM_F32 ? 4 : 2, K = dims->width;
-    if (!aligned_to(dy, es) || !aligned_to(dx, es) || !aligned4(dw) || !aligned4(dbias) || !aligned4(cu_seqlens) ||
-        !aligned16(workspace))
+    if (!aligned_to(dy, es) || !aligned_to(dx, es) || !aligned4(dw) || !aligned4(dbias) || !aligned16(workspace))
         return SSM_ERR_MISALIGNED;
     const Rows ins[] = {{x, dims->tokens, dims->dim * es, dims->x_stride * es}, flat(w, dims->dim * K * 4),
                         flat(bias, dims->dim * 4), flat(cu_seqlens, (dims->sequences + 1) * 4),
@@ -250,7 +258,6 @@ int ssm_conv1d_bwd(const void *x, const float *w, const float *bias, const int32
     if (outputs_clash(ins, outs)) return SSM_ERR_INVALID_ARG;
     p.dy = dy, p.dx = dx, p.dy_stride = dims->dy_stride, p.dx_stride = dims->dx_stride;
     p.partial = static_cast<float *>(workspace), p.dw = dw, p.dbias = dbias;
-    p.seq.cu = cu_seqlens;
     p.tile = conv_bwd_tile(dims->tokens, dims->dim);
     const int64_t tiles = conv_bwd_tiles(dims->tokens, dims->dim);
     const bool vec = vector_rows({x, dy, dx, w, bias}, {dims->x_stride, dims->dy_stride, dims->dx_stride}, dims->dim, dims->act_dtype);
@@ -468,7 +475,7 @@ int ssd_setup(const void *x, const void *dt, const float *dt_bias, const float *
     if (d->tokens < 1 || d->heads < 1 || d->groups < 1 || d->headdim < 1 || d->dstate < 1 || d->slots < 0 || d->heads % d->groups != 0)
         return SSM_ERR_INVALID_ARG;
     if (d->headdim != kSsdP || d->dstate != kSsdN || !dtype_ok(d->act_dtype)) return SSM_ERR_UNSUPPORTED;
-    if (d->tokens > INT32_MAX - kVarQ || d->sequences > INT32_MAX / 4 || d->slots > INT32_MAX || d->heads > 65535) return SSM_ERR_UNSUPPORTED;
+    if (d->tokens > INT32_MAX - kVarQ || d->slots > INT32_MAX || d->heads > 65535) return SSM_ERR_UNSUPPORTED;
     const int64_t inner = d->heads * kSsdP, bc = d->groups * kSsdN;
     if (d->x_stride < inner || d->y_stride < inner || d->dt_stride < d->heads || d->b_stride < bc || d->c_stride < bc)
         return SSM_ERR_INVALID_ARG;
@@ -554,6 +561,7 @@ int ssd_varlen_impl(const void *x, const void *dt, const float *dt_bias, int sof
     if (rc != SSM_OK) return rc;
     if (dims->act_dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
     if (!cu_seqlens || !workspace || dims->sequences < 1) return SSM_ERR_INVALID_ARG;
+    if (dims->sequences > INT32_MAX / 4) return SSM_ERR_UNSUPPORTED;
     // TMA rows and 16-byte stores
     for (const void *q : {x, B, C, static_cast<const void *>(y), static_cast<const void *>(states), static_cast<const void *>(workspace)})
         if (!aligned16(q)) return SSM_ERR_MISALIGNED;
