@@ -118,6 +118,15 @@ def _cuda(x, rank, name):
     return x.device
 
 
+def _size(t, i, rank, name):
+    """t.shape[i] of a tensor that must have `rank` dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != rank:
+        raise ValueError(f"{name} must have {rank} dimensions, got shape {tuple(t.shape)}")
+    return t.shape[i]
+
+
 class _on:
     """The device and the stream of a call; what is allocated meanwhile belongs to that stream."""
     __slots__ = ("device", "stream", "inside")
@@ -149,8 +158,8 @@ def _tables(cu_seqlens, slots, has_initial, device):
     n = cu_seqlens.shape[0] - 1
     pc = _flat(cu_seqlens, torch.int32, device, (n + 1,), "cu_seqlens")
     ps = _flat(slots, torch.int32, device, (n,), "slots")
-    ph = _flat(has_initial, torch.uint8 if has_initial is not None and has_initial.dtype is torch.uint8 else torch.bool, device,
-               (n,), "has_initial")
+    ph = _flat(has_initial, torch.uint8 if getattr(has_initial, "dtype", None) is torch.uint8 else torch.bool, device, (n,),
+               "has_initial")
     return pc, ps, ph, n
 
 
@@ -176,14 +185,14 @@ def ssm_conv1d_fwd(x, conv_w, conv_bias, cu_seqlens, windows=None, slots=None, h
     T, dim = x.shape
     act, f32 = x.dtype, torch.float32
     code = _act_code(x)
-    K = int(conv_w.shape[1])
+    K = _size(conv_w, 1, 2, "conv_w")
     px, xs = _rows(x, dev, "x")
     pw = _flat(conv_w, f32, dev, (dim, K), "conv_w")
     pb = _flat(conv_bias, f32, dev, (dim,), "conv_bias")
     pc, ps, ph, n = _tables(cu_seqlens, slots, has_initial, dev)
     nslots = 0
     if windows is not None:
-        nslots = windows.shape[0]
+        nslots = _size(windows, 0, 3, "windows")
     pwin = _flat(windows, act, dev, (nslots, K - 1, dim), "windows")
     with _on(dev, stream) as sp:
         if out is None:
@@ -203,12 +212,12 @@ def ssm_conv1d_step(windows, x, conv_w, conv_bias, slots=None, silu=True, out=No
     b, dim = x.shape
     act, f32 = x.dtype, torch.float32
     code = _act_code(x)
-    K = int(conv_w.shape[1])
+    K = _size(conv_w, 1, 2, "conv_w")
     px, xs = _rows(x, dev, "x")
     pw = _flat(conv_w, f32, dev, (dim, K), "conv_w")
     pb = _flat(conv_bias, f32, dev, (dim,), "conv_bias")
     ps = _flat(slots, torch.int32, dev, (b,), "slots")
-    nslots = windows.shape[0] if windows is not None else b
+    nslots = _size(windows, 0, 3, "windows") if windows is not None else b
     pwin = _flat(windows, act, dev, (nslots, K - 1, dim), "windows")
     with _on(dev, stream) as sp:
         if out is None:
@@ -227,7 +236,7 @@ def ssm_conv1d_bwd(x, conv_w, conv_bias, cu_seqlens, dy, silu=True, dx=None, str
     T, dim = x.shape
     act, f32 = x.dtype, torch.float32
     code = _act_code(x)
-    K = int(conv_w.shape[1])
+    K = _size(conv_w, 1, 2, "conv_w")
     px, xs = _rows(x, dev, "x")
     pw = _flat(conv_w, f32, dev, (dim, K), "conv_w")
     pb = _flat(conv_bias, f32, dev, (dim,), "conv_bias")
@@ -281,7 +290,7 @@ def ssm_ssd_varlen_fwd(x, dt, dt_bias, softplus, A, B, C, D, cu_seqlens, states=
     px, pdt, pbias, pA, pB, pC, pD, dims = _ssd_args(x, dt, dt_bias, A, B, C, D, dev)
     pc, ps, ph, n = _tables(cu_seqlens, slots, has_initial, dev)
     dims.sequences = n
-    dims.slots = states.shape[0] if states is not None else 0
+    dims.slots = _size(states, 0, 4, "states") if states is not None else 0
     pst = _flat(states, torch.float32, dev, (dims.slots, dims.heads, dims.headdim, dims.dstate), "states")
     lib = get_lib()
     with _on(dev, stream) as sp:
@@ -304,9 +313,7 @@ def ssm_ssd_step(states, x, dt, dt_bias, softplus, A, B, C, D=None, slots=None, 
     padding and is not written."""
     dev = _cuda(x, 3, "x")
     px, pdt, pbias, pA, pB, pC, pD, dims = _ssd_args(x, dt, dt_bias, A, B, C, D, dev)
-    if not isinstance(states, torch.Tensor):
-        raise TypeError("states must be a torch.Tensor")
-    dims.slots = states.shape[0]
+    dims.slots = _size(states, 0, 4, "states")
     pst = _flat(states, torch.float32, dev, (dims.slots, dims.heads, dims.headdim, dims.dstate), "states")
     ps = _flat(slots, torch.int32, dev, (x.shape[0],), "slots")
     with _on(dev, stream) as sp:

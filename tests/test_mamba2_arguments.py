@@ -23,3 +23,27 @@ def test_steps_ignore_the_number_of_sequences(sequences):
                              dt_stride=8, b_stride=256, c_stride=256, y_stride=512, act_dtype=1)
     args = [_p(10), None, _p(1), _p(2), None, 1, _p(3), _p(4), _p(5), None, _p(10)]
     assert lib.ssm_ssd_step(*args, ctypes.byref(dims), None) == 1
+
+
+def test_tables_that_are_no_tensors_or_of_other_types():
+    from selective_state_space_38_b200.mamba2 import _tables
+    cu, cpu = torch.tensor([0, 3, 5], dtype=torch.int32), torch.device("cpu")
+    assert _tables(cu, None, torch.tensor([True, False]), cpu)[3] == 2
+    assert _tables(cu, None, torch.tensor([1, 0], dtype=torch.uint8), cpu)[3] == 2
+    for has_initial in ([True, False], True, torch.tensor([1, 0])):
+        with pytest.raises(TypeError, match="has_initial"):
+            _tables(cu, None, has_initial, cpu)
+    with pytest.raises(ValueError, match="has_initial"):
+        _tables(cu, None, torch.tensor([True]), cpu)
+    with pytest.raises(TypeError, match="slots"):
+        _tables(cu, [0, 1], None, cpu)
+
+
+def test_sizes_of_what_is_no_tensor_or_of_another_rank():
+    from selective_state_space_38_b200.mamba2 import _size
+    assert _size(torch.zeros(6, 4), 1, 2, "conv_w") == 4
+    with pytest.raises(TypeError, match="conv_w"):
+        _size([[0.0] * 4], 1, 2, "conv_w")
+    for shape in ((6,), (6, 1, 4)):
+        with pytest.raises(ValueError, match="conv_w"):
+            _size(torch.zeros(shape), 1, 2, "conv_w")
