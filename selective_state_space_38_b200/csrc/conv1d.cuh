@@ -14,9 +14,9 @@
 // for the K - 1 rows before a tile; the rows of a batch are loaded ahead of
 // their use to keep enough bytes in flight.  Measured, 5376 bf16 channels as slices
 // of wider rows, K = 4, silu: forward of 16117 rows 70 us, 5.0 TB/s, 75 % of the
-// copy rate (the same walk that only copies takes 60 us; the rest is the latency of
-// the 51 instructions a row and thread at 24 warps an SM: more warps with fewer rows
-// ahead were slower, 77); gradients of 16384 rows 135 us, 3.9 TB/s, 60 % (some 100
+// copy rate, some 5 us of it the windows' kernel (the same walk that only copies takes
+// 60 us; the rest is the latency of the 51 instructions a row and thread at 24 warps
+// an SM: more warps with fewer rows ahead were slower, 77); gradients of 16384 rows 135 us, 3.9 TB/s, 60 % (some 100
 // instructions a row and thread, whose 128 registers leave 16 warps an SM; issue slots
 // and FMA pipe at half of their rates); one token for 256 rows 10 us, launch included.
 #pragma once

@@ -136,9 +136,9 @@ struct Row {
     }
 };
 
-// 16 bytes global -> shared without a register round trip (bytes = 0: zeros, nothing read).
-__device__ __forceinline__ void copy16_async(void *dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+// 16 bytes global -> shared without a register round trip.
+__device__ __forceinline__ void copy16_async(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

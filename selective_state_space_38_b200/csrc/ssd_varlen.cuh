@@ -39,10 +39,11 @@
 // 128 x 128 x 128, 512 cycles of the tensor pipe each at 8192 bf16 flops a cycle;
 // shared memory carries about 640 KB for them and their operands, 5000 cycles at
 // 128 bytes a cycle, and bounds it together with the chain from a chunk's state to the
-// next one's (about 8600 cycles are measured).  4 x 4096 tokens of 80 heads in one
-// group take 190 us: 342 TFLOP/s, 20 % of the dense rate, 1.9 TB/s; 20 ragged prompts
-// of 24 heads 81 us; one of 32768 tokens and 24 heads 193 us.  One CTA per SM.  One warp issues the TMA loads and one the MMAs,
-// one walks the work list, one forms the chunks' running sums and factors, and
+// next one's (about 8600 cycles are measured).  Replayed in a graph, 4 x 4096 tokens of
+// 80 heads in one group take 191 us: 340 TFLOP/s, 20 % of the dense rate, 1.9 TB/s; 20
+// ragged prompts of 24 heads 81 us; one of 32768 tokens and 24 heads 190 us (called one
+// by one 203, 81 and 196).  One CTA per SM.  One warp issues the TMA loads and one the
+// MMAs, one walks the work list, one forms the chunks' running sums and factors, and
 // sixteen epilogue warps work in two halves: eight on the state (S and its operand,
 // the parts of w x), eight on the output (y), so that a chunk's y is written while the
 // next one's state and operands are formed; C B^T takes its factors from all sixteen
@@ -55,8 +56,8 @@
 // range is then the end of one chain (its tail), whole chains, and the start of
 // another (its head): the CTA walks the head first and hands its state on, the tail
 // last, from the state that the CTA before handed on after its own head, so that the
-// wait normally finds it there.  Whole chains, from a queue, the longer sequences'
-// first, when some are longer than that.  And two passes over segments of the
+// wait normally finds it there.  Whole chains, from a queue, when some are longer than
+// that: those of sequences of more than one segment first, in packed order.  And two passes over segments of the
 // sequences when the longest chain would leave the other SMs idle: the segments' own
 // states first, from zeros and without outputs, all at once, then the states at their
 // starts (ssd_varlen_combine_kernel), then every segment by itself.  In that last pass
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(SUMMARY ? kVarSummaryThreads : kVarThreads, 1)
         // ---- the work list: one item ahead of the table warp ------------------------------
         const int HG = p.heads / p.groups, pairs_per_group = p.pairs / p.groups;
         uint32_t k = 0;  // items handed on
-        auto hand_on = [&](bool valid, int n, int pair, int64_t first, int64_t stop, const float *src, float *dst, uint32_t *flag,
+        auto hand_on = [&](bool valid, int pair, int64_t first, int64_t stop, const float *src, float *dst, uint32_t *flag,
                            float *decay) -> bool {
             if (k > 0 && !wait(bTaken, (k - 1) & 1u)) return false;
             if (lane == 0) {
@@ -675,13 +676,13 @@ __global__ void __launch_bounds__(SUMMARY ? kVarSummaryThreads : kVarThreads, 1)
                 const int h0 = head_of(pair);
                 if constexpr (SUMMARY) {
                     const int64_t w = (window + 1) * p.heads + h0;
-                    ok = hand_on(true, n, pair, first, stop, nullptr, p.work.carry + w * (kSsdP * kSsdN), nullptr, p.work.decay + w);
+                    ok = hand_on(true, pair, first, stop, nullptr, p.work.carry + w * (kSsdP * kSsdN), nullptr, p.work.decay + w);
                 } else {
                     const float *src;
                     float *state = cache(n, pair, &src);
                     if (seg > 0) src = p.work.carry + (window * p.heads + h0) * (kSsdP * kSsdN);
                     else if (src && stop < end) src = p.work.start + (static_cast<int64_t>(several_before(n)) * p.heads + h0) * (kSsdP * kSsdN);
-                    ok = hand_on(true, n, pair, first, stop, src, stop < end ? nullptr : state, nullptr, nullptr);
+                    ok = hand_on(true, pair, first, stop, src, stop < end ? nullptr : state, nullptr, nullptr);
                 }
             }
         } else {
@@ -721,7 +722,7 @@ __global__ void __launch_bounds__(SUMMARY ? kVarSummaryThreads : kVarThreads, 1)
                         dst = p.work.carry + static_cast<int64_t>(order) * kVarHeads * (kSsdP * kSsdN);
                         flag = p.work.flags + order;
                     }
-                    return hand_on(true, a.n, a.pair, begin + static_cast<int64_t>(c0) * kVarQ,
+                    return hand_on(true, a.pair, begin + static_cast<int64_t>(c0) * kVarQ,
                                    min(begin + static_cast<int64_t>(c1) * kVarQ, end), src, dst, flag, nullptr);
                 };
                 if (from.n == to.n && from.pair == to.pair) {
@@ -741,7 +742,7 @@ __global__ void __launch_bounds__(SUMMARY ? kVarSummaryThreads : kVarThreads, 1)
                 }
             }
         }
-        hand_on(false, 0, 0, 0, 0, nullptr, nullptr, nullptr, nullptr);  // (after a failure too, for those who can still hear it)
+        hand_on(false, 0, 0, 0, nullptr, nullptr, nullptr, nullptr);  // (after a failure too, for those who can still hear it)
         __syncwarp();
     } else if (warp >= kTableWarp && warp < kTableWarp + kTables) {
         // ---- the tables: running sums and factors.  Half a warp per head, eight rows per lane
